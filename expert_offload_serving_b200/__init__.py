@@ -22,6 +22,11 @@ STATUS_NAMES = ["MOE_OK", "MOE_ERR_INVALID_ARG", "MOE_ERR_UNSUPPORTED", "MOE_ERR
 MOE_W_BF16, MOE_W_MXFP4, MOE_W_NVFP4 = 0, 1, 2
 FORMATS = {"bf16": MOE_W_BF16, "mxfp4": MOE_W_MXFP4, "nvfp4": MOE_W_NVFP4}
 MOE_FFN_ACT_NVFP4 = 1
+MOE_W_INT4 = 3
+LINEAR_FORMATS = {"mxfp4": MOE_W_MXFP4, "nvfp4": MOE_W_NVFP4, "int4": MOE_W_INT4}
+MOE_DT_F32, MOE_DT_BF16, MOE_DT_F16 = 0, 1, 2
+DTYPES = {torch.float32: MOE_DT_F32, torch.bfloat16: MOE_DT_BF16, torch.float16: MOE_DT_F16}
+MOE_LINEAR_SWIGLU, MOE_LINEAR_ACCUMULATE = 1, 2
 
 
 class MoeError(RuntimeError):
@@ -36,9 +41,15 @@ class moe_shape(ctypes.Structure):
                 ("fmt", ctypes.c_int32)]
 
 
+class moe_linear_shape(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int32), ("K", ctypes.c_int32), ("fmt", ctypes.c_int32),
+                ("group", ctypes.c_int32), ("scale_type", ctypes.c_int32)]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _SZ = ctypes.c_size_t
+_I64 = ctypes.c_int64
 _SIGS = {
     "moe_abi_version": (_I, []),
     "moe_last_error": (ctypes.c_char_p, []),
@@ -69,6 +80,11 @@ _SIGS = {
     "moe_cache_query": (_I, [_P, _P, _P, _P]),
     "moe_cache_destroy": (_I, [_P]),
     "moe_check_status": (_I, [_P, _P]),
+    "moe_linear_w4": (_I, [moe_linear_shape, _P, _P, _P, ctypes.c_float, _P, _I, _I64, _I, _P, _I, _I64, _I, _P]),
+    "moe_balance_loss_workspace_bytes": (_SZ, [_I, _I, _I]),
+    "moe_balance_loss": (_I, [_P, _I, _I, _P, _I, _P, _I, _P, _P, _P, _P, _P, _P, _SZ, _P, _P]),
+    "moe_router_backward": (_I, [_P, _I, _I, _P, _P, _P, _I, _P, _I, _P, _P, _P, _P, _P, _P, _P]),
+    "moe_combine_backward": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P]),
 }
 
 _lib = None
@@ -272,6 +288,128 @@ def moe_layer_forward(s: moe_shape, logits, x, k: int, idx, gate, offsets, perm,
                                    _ptr(inv_perm), _ptr(scratch), sb, _ptr(slot_of_expert), _ptr(slot_pool),
                                    n_slots, _ptr(y_perm), flags, _ptr(workspace), wb, _ptr(host_partial),
                                    _ptr(out), _ptr(dev_status), _stream(stream)))
+
+
+def _here(*tensors):
+    """The calls below run on the current device: their tensors must live there."""
+    cur = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != cur:
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{cur}")
+
+
+def _rows(name, t, n, width):
+    """A CUDA matrix of n rows of `width` elements, any distance apart; returns it."""
+    if not t.is_cuda or t.dim() != 2 or t.shape[0] != n or t.shape[1] != width or (width > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: expected a CUDA [{n}, {width}] tensor with contiguous rows, got {t.dtype} "
+                         f"{tuple(t.shape)} with strides {t.stride()} on {t.device}")
+    if n > 1 and t.stride(0) < width:
+        raise ValueError(f"{name}: rows overlap (stride {t.stride(0)} < {width})")
+    return t.stride(0) if n > 1 else max(t.stride(0), width)
+
+
+def moe_linear_w4(x, codes, scales, out, fmt="int4", group: int = 128, zeros=None, tensor_scale: float = 1.0,
+                  swiglu: bool = False, accumulate: bool = False, stream=None):
+    """out = x W^T (+ out) with the 4-bit weights codes [N, K/2] uint8 (element
+    2i in the low nibble) and scales [N, ceil(K/group)]: fmt "int4" (scales
+    fp32/bf16/fp16, zeros uint8 of the same shape or None for 8), "mxfp4" or
+    "nvfp4" (scales uint8, group 32 or 16).  x [T, K] bf16 or fp16, out [T, N] of
+    x's type or fp32; rows of both may be any distance apart.  swiglu: out
+    [T, N/2] = silu(h) * u of W's two row halves."""
+    T, K = x.shape
+    N = codes.shape[0]
+    f = LINEAR_FORMATS[fmt]
+    G = -(-K // group)
+    _dev("codes", codes, N * (K // 2), torch.uint8)
+    _dev("scales", scales, N * G, torch.uint8 if f != MOE_W_INT4 else scales.dtype)
+    _dev("zeros", zeros, N * G, torch.uint8)
+    for name, t, want in (("codes", codes, (N, K // 2)), ("scales", scales, (N, G)), ("zeros", zeros, (N, G))):
+        if t is not None and tuple(t.shape) != want:
+            raise ValueError(f"{name}: expected shape {want} for K={K}, group={group}, got {tuple(t.shape)}")
+    if f == MOE_W_INT4 and scales.dtype not in DTYPES:
+        raise ValueError(f"scales: expected float32, bfloat16 or float16, got {scales.dtype}")
+    if x.dtype not in DTYPES or out.dtype not in DTYPES:
+        raise ValueError(f"x {x.dtype}, out {out.dtype}: expected bfloat16 or float16, and that or float32")
+    ldx, ldy = _rows("x", x, T, K), _rows("out", out, T, N // 2 if swiglu else N)
+    _here(x, codes, scales, zeros, out)
+    s = moe_linear_shape(N, K, f, group, DTYPES.get(scales.dtype, MOE_DT_F32))
+    if T == 1:
+        ldx = (ldx + 7) // 8 * 8          # the distance of rows that are not there
+    _check(lib().moe_linear_w4(s, _ptr(codes), _ptr(scales), _ptr(zeros), tensor_scale, _ptr(x), DTYPES[x.dtype], ldx,
+                               T, _ptr(out), DTYPES[out.dtype], ldy,
+                               (MOE_LINEAR_SWIGLU if swiglu else 0) | (MOE_LINEAR_ACCUMULATE if accumulate else 0),
+                               _stream(stream)))
+
+
+def _batch(logits, idx, seq_offsets, mask):
+    T, E = logits.shape
+    k = idx.shape[1]
+    S = 1 if seq_offsets is None else seq_offsets.numel() - 1
+    _dev("logits", logits, T * E, torch.float32)
+    _dev("idx", idx, T * k, torch.int32)
+    _dev("seq_offsets", seq_offsets, S + 1, torch.int32)
+    if mask is not None:
+        _dev("mask", mask, T, torch.bool if mask.dtype == torch.bool else torch.uint8)
+    return T, E, k, S
+
+
+def moe_balance_loss_workspace_bytes(T: int, E: int, S: int = 1) -> int:
+    return lib().moe_balance_loss_workspace_bytes(T, E, S)
+
+
+def moe_balance_loss(logits, idx, loss, counts, prob, coef, workspace, seq_offsets=None, mask=None,
+                     dev_status=None, stream=None):
+    """loss [2] = (balance loss, z-loss), counts [S, E] int32, prob [S, E] and
+    coef [S + 1] of the routing idx [T, k] of logits [T, E]; seq_offsets int32
+    [S + 1] (None: one sequence), mask [T] bool or uint8 (None: every token)."""
+    T, E, k, S = _batch(logits, idx, seq_offsets, mask)
+    _dev("loss", loss, 2, torch.float32)
+    _dev("counts", counts, S * E, torch.int32)
+    _dev("prob", prob, S * E, torch.float32)
+    _dev("coef", coef, S + 1, torch.float32)
+    _dev("workspace", workspace, 0, torch.uint8)
+    _dev("dev_status", dev_status, 1, torch.int32)
+    _here(logits, idx, loss, counts, prob, coef, workspace, seq_offsets, mask, dev_status)
+    _check(lib().moe_balance_loss(_ptr(logits), T, E, _ptr(idx), k, _ptr(seq_offsets), S, _ptr(mask), _ptr(loss),
+                                  _ptr(counts), _ptr(prob), _ptr(coef), _ptr(workspace), workspace.numel(),
+                                  _ptr(dev_status), _stream(stream)))
+
+
+def moe_router_backward(logits, idx, dlogits, gate=None, dgate=None, counts=None, coef=None, dloss=None,
+                        seq_offsets=None, mask=None, dev_status=None, stream=None):
+    """dlogits [T, E] of the gates (dgate [T, k]; None: no such term) and of the
+    losses (dloss [2], with counts and coef of moe_balance_loss; None: none)."""
+    T, E, k, S = _batch(logits, idx, seq_offsets, mask)
+    _dev("dlogits", dlogits, T * E, torch.float32)
+    _dev("gate", gate, T * k, torch.float32)
+    _dev("dgate", dgate, T * k, torch.float32)
+    _dev("counts", counts, S * E, torch.int32)
+    _dev("coef", coef, S + 1, torch.float32)
+    _dev("dloss", dloss, 2, torch.float32)
+    _dev("dev_status", dev_status, 1, torch.int32)
+    _here(logits, idx, dlogits, gate, dgate, counts, coef, dloss, seq_offsets, mask, dev_status)
+    _check(lib().moe_router_backward(_ptr(logits), T, E, _ptr(idx), _ptr(gate), _ptr(dgate), k, _ptr(seq_offsets), S,
+                                     _ptr(mask), _ptr(counts), _ptr(coef), _ptr(dloss), _ptr(dlogits),
+                                     _ptr(dev_status), _stream(stream)))
+
+
+def moe_combine_backward(y_perm, idx, gate, inv_perm, slot_of_expert, dout, E: int, dgate, dy_perm=None, stream=None):
+    """dgate [T, k] and, if wanted, dy_perm [T*k, d] from dout [T, d], for the
+    pairs moe_combine_merge adds (the other pairs' dgate is 0, their dy_perm
+    rows stay as they are)."""
+    T, k = idx.shape
+    d = dout.shape[1]
+    _dev("y_perm", y_perm, T * k * d, torch.float32)
+    _dev("idx", idx, T * k, torch.int32)
+    _dev("gate", gate, T * k, torch.float32)
+    _dev("inv_perm", inv_perm, T * k, torch.int32)
+    _dev("slot_of_expert", slot_of_expert, E, torch.int32)
+    _dev("dout", dout, T * d, torch.float32)
+    _dev("dgate", dgate, T * k, torch.float32)
+    _dev("dy_perm", dy_perm, T * k * d, torch.float32)
+    _here(y_perm, idx, gate, inv_perm, slot_of_expert, dout, dgate, dy_perm)
+    _check(lib().moe_combine_backward(_ptr(y_perm), _ptr(idx), _ptr(gate), _ptr(inv_perm), _ptr(slot_of_expert),
+                                      _ptr(dout), T, k, d, E, _ptr(dgate), _ptr(dy_perm), _stream(stream)))
 
 
 def moe_split_misses(misses, tokens_per_expert, q=None, bw_pcie=0.0, bw_host=0.0):

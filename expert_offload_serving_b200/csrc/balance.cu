@@ -1,0 +1,466 @@
+// The balance loss with its per-expert counts, and the router's gradient.
+//
+// With f = counts and P = the mean softmax probability of a sequence,
+//   loss[0] = 1/S' sum_s E/(k n_s) sum_e f_e P_e,   loss[1] = 1/n sum_t lse_t^2,
+//   dlogits = dloss[0] coef_s p (f - <f, p>) + dloss[1] 2 coef_S lse p
+//           + (on the chosen experts) gate (dgate - <gate, dgate>).
+//
+// Forward: one pass over the logits.  The tokens are cut into tiles, one CTA
+// each; a warp holds a token's E logits in registers (lane l: experts l, l+32,
+// ...) and adds its probabilities to running sums in registers.  A tile writes
+// one partial per sequence that it touches, at row (tile + sequence): both grow
+// along the tokens, so the rows are distinct and those of one sequence are
+// consecutive.  A second kernel adds them up, one CTA per (sequence, 32
+// experts), and its last CTA forms the loss.  Every sum has a fixed order; the
+// atomics only count (integers) or hand out tickets.
+//
+// Backward: one warp per token, nothing kept from the forward but counts and
+// coef: the softmax is formed again from the logits, which costs no traffic
+// (the row is read anyway).  Bound by HBM: 4 E bytes in, 4 E out per token.
+#include <climits>
+#include <cmath>
+
+#include "common.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kMaxTiles = 592;      // 4 CTAs on each of 148 SMs
+constexpr int kMaxS = 1 << 20;
+
+struct BalanceLayout {
+  int tile_tokens, tiles, eblocks;
+  size_t rows, p, c, n, z, q, sn, sz, ticket, bytes;
+};
+
+BalanceLayout balance_layout(int T, int E, int S) {
+  BalanceLayout L{};
+  int C = (T + kMaxTiles - 1) / kMaxTiles;
+  C = ((C < 1 ? 1 : C) + kWarps - 1) / kWarps * kWarps;
+  L.tile_tokens = C;
+  L.tiles = T > 0 ? (T + C - 1) / C : 1;
+  L.eblocks = (E + 31) / 32;
+  L.rows = static_cast<size_t>(L.tiles) + S;
+  size_t at = 0;
+  auto take = [&at](size_t bytes) {
+    const size_t o = at;
+    at += (bytes + 15) / 16 * 16;
+    return o;
+  };
+  L.p = take(L.rows * E * 4);
+  L.c = take(L.rows * E * 4);
+  L.n = take(L.rows * 4);
+  L.z = take(L.rows * 4);
+  L.q = take(static_cast<size_t>(S) * L.eblocks * 8);
+  L.sn = take(static_cast<size_t>(S) * 4);
+  L.sz = take(static_cast<size_t>(S) * 8);
+  L.ticket = take(4);
+  L.bytes = at;
+  return L;
+}
+
+struct BalanceWs {
+  float* p;        // [rows][E] sums of probabilities
+  int32_t* c;      // [rows][E] pairs
+  int32_t* n;      // [rows] tokens
+  float* z;        // [rows] sums of lse^2
+  double* q;       // [S][eblocks] sums of counts * sum of probabilities
+  int32_t* sn;     // [S]
+  double* sz;      // [S]
+  unsigned* ticket;
+};
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+  return v;
+}
+template <typename V>
+__device__ __forceinline__ V warp_sum(V v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
+
+// Offset i, kept within [0, T] so that no bad value leads an access astray.
+__device__ __forceinline__ int offset_at(const int32_t* off, int i, int T) {
+  const int v = __ldg(off + i);
+  return v < 0 ? 0 : (v > T ? T : v);
+}
+
+// The first sequence that ends after token t (S if none): the one that holds t, if any does.
+__device__ __forceinline__ int sequence_of(const int32_t* off, int S, int T, int t) {
+  int lo = 0, hi = S;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (offset_at(off, mid + 1, T) > t) hi = mid;
+    else lo = mid + 1;
+  }
+  return lo;
+}
+
+// The softmax of a row held VPL values a lane: v becomes the probabilities (all
+// 0 for a row of -inf), and the row's logsumexp is returned (0 for such a row).
+template <int VPL>
+__device__ __forceinline__ float softmax_row(float (&v)[VPL]) {
+  float top = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) top = fmaxf(top, v[j]);
+  top = warp_max(top);
+  const bool empty = top == -INFINITY;
+  float sum = 0.f;
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) {
+    v[j] = empty ? 0.f : expf(v[j] - top);
+    sum += v[j];
+  }
+  sum = warp_sum(sum);
+  if (empty) return 0.f;
+  const float inv = 1.f / sum;
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) v[j] *= inv;
+  return top + logf(sum);
+}
+
+template <int VPL>
+__device__ __forceinline__ void load_row(const float* __restrict__ row, int E, int lane, float (&v)[VPL]) {
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) {
+    const int e = lane + 32 * j;
+    v[j] = e < E ? __ldg(row + e) : -INFINITY;
+  }
+}
+
+template <int VPL>
+__global__ void __launch_bounds__(kThreads) balance_partial_kernel(
+    const float* __restrict__ logits, int T, int E, const int32_t* __restrict__ idx, int k,
+    const int32_t* __restrict__ seq, int S, const uint8_t* __restrict__ mask, int tile_tokens, BalanceWs ws,
+    int32_t* status) {
+  extern __shared__ float smem[];
+  float* wsum = smem;                                        // [kWarps][E]
+  int* hist = reinterpret_cast<int*>(smem + kWarps * E);     // [E]
+  __shared__ float wz[kWarps];
+  __shared__ int wn[kWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *ws.ticket = 0;
+  for (int e = threadIdx.x; e < E; e += kThreads) hist[e] = 0;
+  const int t0 = blockIdx.x * tile_tokens;
+  const int t1 = min(T, t0 + tile_tokens);
+  for (int s = seq == nullptr ? 0 : sequence_of(seq, S, T, t0); s < S; ++s) {
+    const int a = seq == nullptr ? 0 : offset_at(seq, s, T), b = seq == nullptr ? T : offset_at(seq, s + 1, T);
+    if (a >= t1) break;
+    const int lo = max(a, t0), hi = min(b, t1);
+    if (lo >= hi) continue;
+    __syncthreads();                                         // hist is clear, wsum may be written
+    float acc[VPL], z = 0.f;
+    int n = 0;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) acc[j] = 0.f;
+    for (int t = lo + warp; t < hi; t += kWarps) {
+      if (mask != nullptr && __ldg(mask + t) == 0) continue;
+      float v[VPL];
+      load_row<VPL>(logits + static_cast<size_t>(t) * E, E, lane, v);
+      if (lane < k) {
+        const int e = __ldg(idx + static_cast<size_t>(t) * k + lane);
+        if (e >= 0 && e < E) atomicAdd(&hist[e], 1);
+        else report(status, MOE_ERR_DEVICE);
+      }
+      const float lse = softmax_row<VPL>(v);
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) acc[j] += v[j];
+      z = fmaf(lse, lse, z);
+      ++n;
+    }
+#pragma unroll
+    for (int j = 0; j < VPL; ++j)
+      if (lane + 32 * j < E) wsum[warp * E + lane + 32 * j] = acc[j];
+    if (lane == 0) {
+      wz[warp] = z;
+      wn[warp] = n;
+    }
+    __syncthreads();
+    const size_t row = static_cast<size_t>(blockIdx.x) + s;
+    for (int e = threadIdx.x; e < E; e += kThreads) {
+      float p = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) p += wsum[w * E + e];
+      ws.p[row * E + e] = p;
+      ws.c[row * E + e] = hist[e];
+      hist[e] = 0;
+    }
+    if (threadIdx.x == 0) {
+      float zs = 0.f;
+      int ns = 0;
+      for (int w = 0; w < kWarps; ++w) {
+        zs += wz[w];
+        ns += wn[w];
+      }
+      ws.z[row] = zs;
+      ws.n[row] = ns;
+    }
+  }
+}
+
+// Sum over the block in a fixed order; every thread gets it.
+template <typename V>
+__device__ V block_sum(V v, V* sh) {
+  v = warp_sum(v);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+  __syncthreads();
+  V s = 0;
+  for (int w = 0; w < kWarps; ++w) s += sh[w];
+  return s;
+}
+
+__global__ void __launch_bounds__(kThreads) balance_finish_kernel(
+    int T, int E, int k, const int32_t* __restrict__ seq, int S, int tile_tokens, int eblocks, BalanceWs ws,
+    float* __restrict__ loss, int32_t* __restrict__ counts, float* __restrict__ prob, float* __restrict__ coef,
+    int32_t* status) {
+  __shared__ double shd[kWarps];
+  __shared__ int shi[kWarps];
+  __shared__ double wp[kWarps][32];
+  __shared__ int wc[kWarps][32];
+  __shared__ bool last;
+  const int s = blockIdx.x, eb = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int e = eb * 32 + lane;
+  int a = 0, b = T;
+  if (seq != nullptr) {
+    a = offset_at(seq, s, T);
+    b = offset_at(seq, s + 1, T);
+    if (threadIdx.x == 0 && eb == 0 && (a > b || a != __ldg(seq + s) || b != __ldg(seq + s + 1)))
+      report(status, MOE_ERR_DEVICE);
+  }
+  // the rows of this sequence (none if it is empty)
+  const size_t r0 = static_cast<size_t>(a / tile_tokens) + s;
+  const int rows = a < b ? (b - 1) / tile_tokens - a / tile_tokens + 1 : 0;
+  int n = 0;
+  double z = 0;
+  for (int r = threadIdx.x; r < rows; r += kThreads) {
+    n += ws.n[r0 + r];
+    z += ws.z[r0 + r];
+  }
+  n = block_sum(n, shi);
+  z = block_sum(z, shd);
+  double p = 0;
+  int c = 0;
+  if (e < E)
+    for (int r = warp; r < rows; r += kWarps) {
+      p += ws.p[(r0 + r) * E + e];
+      c += ws.c[(r0 + r) * E + e];
+    }
+  wp[warp][lane] = p;
+  wc[warp][lane] = c;
+  __syncthreads();
+  if (warp == 0) {
+    p = 0;
+    c = 0;
+    for (int w = 0; w < kWarps; ++w) {
+      p += wp[w][lane];
+      c += wc[w][lane];
+    }
+    if (e < E) {
+      counts[static_cast<size_t>(s) * E + e] = c;
+      prob[static_cast<size_t>(s) * E + e] = n > 0 ? static_cast<float>(p / n) : 0.f;
+    }
+    const double q = warp_sum(e < E ? p * c : 0.0);
+    if (lane == 0) {
+      ws.q[static_cast<size_t>(s) * eblocks + eb] = q;
+      if (eb == 0) {
+        ws.sn[s] = n;
+        ws.sz[s] = z;
+      }
+      __threadfence();
+      last = atomicAdd(ws.ticket, 1u) == static_cast<unsigned>(S) * eblocks - 1;
+    }
+  }
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  // the last CTA: every other one's sums are visible
+  int some = 0;
+  long long total = 0;
+  double zall = 0, ball = 0;
+  for (int i = threadIdx.x; i < S; i += kThreads) {
+    const int ni = __ldcg(ws.sn + i);
+    some += ni > 0;
+    total += ni;
+    zall += __ldcg(ws.sz + i);
+    if (ni > 0) {
+      double q = 0;
+      for (int j = 0; j < eblocks; ++j) q += __ldcg(ws.q + static_cast<size_t>(i) * eblocks + j);
+      ball += q * E / (static_cast<double>(k) * ni * ni);
+    }
+  }
+  some = block_sum(some, shi);
+  const int all = block_sum(static_cast<int>(total), shi);     // <= T
+  zall = block_sum(zall, shd);
+  ball = block_sum(ball, shd);
+  for (int i = threadIdx.x; i < S; i += kThreads) {
+    const int ni = __ldcg(ws.sn + i);
+    coef[i] = ni > 0 ? static_cast<float>(E / (static_cast<double>(k) * ni * ni * some)) : 0.f;
+  }
+  if (threadIdx.x == 0) {
+    coef[S] = 1.f / static_cast<float>(all > 0 ? all : 1);
+    loss[0] = some > 0 ? static_cast<float>(ball / some) : 0.f;
+    loss[1] = all > 0 ? static_cast<float>(zall / all) : 0.f;
+  }
+}
+
+template <int VPL>
+__global__ void __launch_bounds__(kThreads) router_backward_kernel(
+    const float* __restrict__ logits, int T, int E, const int32_t* __restrict__ idx, const float* __restrict__ gate,
+    const float* __restrict__ dgate, int k, const int32_t* __restrict__ seq, int S, const uint8_t* __restrict__ mask,
+    const int32_t* __restrict__ counts, const float* __restrict__ coef, const float* __restrict__ dloss,
+    float* __restrict__ dlogits, int32_t* status) {
+  const int lane = threadIdx.x & 31;
+  const int t = static_cast<int>((blockIdx.x * static_cast<long long>(kThreads) + threadIdx.x) >> 5);
+  if (t >= T) return;
+  float d[VPL];
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) d[j] = 0.f;
+  int s = 0;
+  bool live = mask == nullptr || __ldg(mask + t) != 0;
+  if (live && seq != nullptr) {
+    s = sequence_of(seq, S, T, t);
+    live = s < S && offset_at(seq, s, T) <= t;
+  }
+  if (live && dloss != nullptr) {
+    load_row<VPL>(logits + static_cast<size_t>(t) * E, E, lane, d);
+    const float lse = softmax_row<VPL>(d);
+    const float cb = __ldg(dloss) * __ldg(coef + s), cz = 2.f * __ldg(dloss + 1) * __ldg(coef + S) * lse;
+    const int32_t* crow = counts + static_cast<size_t>(s) * E;
+    float f[VPL], dot = 0.f;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) {
+      const int e = lane + 32 * j;
+      f[j] = e < E ? static_cast<float>(__ldg(crow + e)) : 0.f;
+      dot = fmaf(f[j], d[j], dot);
+    }
+    dot = warp_sum(dot);
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) d[j] *= fmaf(cb, f[j] - dot, cz);
+  }
+  if (live && dgate != nullptr) {
+    const bool on = lane < k;
+    const size_t p = static_cast<size_t>(t) * k + lane;
+    const float g = on ? __ldg(gate + p) : 0.f, dg = on ? __ldg(dgate + p) : 0.f;
+    int e = on ? __ldg(idx + p) : -1;
+    if (on && (e < 0 || e >= E)) {
+      report(status, MOE_ERR_DEVICE);
+      e = -1;
+    }
+    const float v = g * (dg - warp_sum(on ? g * dg : 0.f));
+    for (int i = 0; i < k; ++i) {
+      const int ei = __shfl_sync(kFull, e, i);
+      const float vi = __shfl_sync(kFull, v, i);
+#pragma unroll
+      for (int j = 0; j < VPL; ++j)
+        if (lane + 32 * j == ei) d[j] += vi;
+    }
+  }
+  float* row = dlogits + static_cast<size_t>(t) * E;
+#pragma unroll
+  for (int j = 0; j < VPL; ++j)
+    if (lane + 32 * j < E) row[lane + 32 * j] = d[j];
+}
+
+moe_status check_sequences(int T, int E, int k, const int32_t* seq, int S) {
+  MOE_REQUIRE(T >= 0, "T=%d < 0", T);
+  MOE_REQUIRE(E >= 1 && E <= 1024, "E=%d outside [1, 1024]", E);
+  MOE_REQUIRE(k >= 1 && k <= E && k <= 32, "k=%d outside [1, min(E, 32)]", k);
+  MOE_REQUIRE(T <= (1 << 24) / k, "T*k too large");
+  MOE_REQUIRE(S >= 1 && S <= kMaxS, "S=%d outside [1, %d]", S, kMaxS);
+  MOE_REQUIRE(seq != nullptr || S == 1, "S=%d sequences need seq_offsets", S);
+  MOE_REQUIRE(aligned(seq, 4), "misaligned seq_offsets");
+  return MOE_OK;
+}
+
+// f(VPL constant): the number of experts a lane holds for E experts.
+template <typename F>
+cudaError_t with_vpl(int E, F f) {
+  if (E <= 32) return f(std::integral_constant<int, 1>());
+  if (E <= 64) return f(std::integral_constant<int, 2>());
+  if (E <= 128) return f(std::integral_constant<int, 4>());
+  if (E <= 256) return f(std::integral_constant<int, 8>());
+  if (E <= 512) return f(std::integral_constant<int, 16>());
+  return f(std::integral_constant<int, 32>());
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" size_t moe_balance_loss_workspace_bytes(int T, int E, int S) {
+  if (T < 0 || T > (1 << 24) || E < 1 || E > 1024 || S < 1 || S > kMaxS) return 0;
+  return balance_layout(T, E, S).bytes;
+}
+
+extern "C" moe_status moe_balance_loss(const float* logits, int T, int E, const int32_t* idx, int k,
+                                       const int32_t* seq_offsets, int S, const uint8_t* mask, float* loss,
+                                       int32_t* counts, float* prob, float* coef, void* workspace, size_t ws_bytes,
+                                       int32_t* dev_status, cudaStream_t stream) {
+  clear_error();
+  moe_status st = check_sequences(T, E, k, seq_offsets, S);
+  if (st != MOE_OK) return st;
+  MOE_REQUIRE(loss && counts && prob && coef && workspace && (T == 0 || (logits && idx)), "null pointer");
+  MOE_REQUIRE(aligned(logits, 4) && aligned(idx, 4) && aligned(loss, 4) && aligned(counts, 4) && aligned(prob, 4) &&
+                  aligned(coef, 4), "misaligned pointer");
+  MOE_REQUIRE(aligned(workspace, 16), "workspace must be 16-byte aligned");
+  const BalanceLayout L = balance_layout(T, E, S);
+  if (ws_bytes < L.bytes)
+    return fail(MOE_ERR_CAPACITY, "moe_balance_loss needs %zu bytes of workspace, got %zu", L.bytes, ws_bytes);
+  DeviceInfo dev;
+  st = current_device(&dev);
+  if (st != MOE_OK) return st;
+  char* w = static_cast<char*>(workspace);
+  BalanceWs ws;
+  ws.p = reinterpret_cast<float*>(w + L.p);
+  ws.c = reinterpret_cast<int32_t*>(w + L.c);
+  ws.n = reinterpret_cast<int32_t*>(w + L.n);
+  ws.z = reinterpret_cast<float*>(w + L.z);
+  ws.q = reinterpret_cast<double*>(w + L.q);
+  ws.sn = reinterpret_cast<int32_t*>(w + L.sn);
+  ws.sz = reinterpret_cast<double*>(w + L.sz);
+  ws.ticket = reinterpret_cast<unsigned*>(w + L.ticket);
+  const size_t smem = static_cast<size_t>(kWarps + 1) * E * 4;     // <= 36 KB
+  const cudaError_t err = with_vpl(E, [&](auto vpl) {
+    balance_partial_kernel<decltype(vpl)::value><<<L.tiles, kThreads, smem, stream>>>(
+        logits, T, E, idx, k, seq_offsets, S, mask, L.tile_tokens, ws, dev_status);
+    return cudaGetLastError();
+  });
+  if (err != cudaSuccess) return fail(MOE_ERR_CUDA, "balance_partial launch: %s", cudaGetErrorString(err));
+  balance_finish_kernel<<<dim3(S, L.eblocks), kThreads, 0, stream>>>(T, E, k, seq_offsets, S, L.tile_tokens,
+                                                                     L.eblocks, ws, loss, counts, prob, coef,
+                                                                     dev_status);
+  MOE_LAUNCH_CHECK("balance_finish_kernel");
+  return MOE_OK;
+}
+
+extern "C" moe_status moe_router_backward(const float* logits, int T, int E, const int32_t* idx, const float* gate,
+                                          const float* dgate, int k, const int32_t* seq_offsets, int S,
+                                          const uint8_t* mask, const int32_t* counts, const float* coef,
+                                          const float* dloss, float* dlogits, int32_t* dev_status,
+                                          cudaStream_t stream) {
+  clear_error();
+  moe_status st = check_sequences(T, E, k, seq_offsets, S);
+  if (st != MOE_OK || T == 0) return st;
+  MOE_REQUIRE(dlogits != nullptr, "null dlogits");
+  MOE_REQUIRE(dloss == nullptr || (logits && counts && coef), "dloss needs logits, counts and coef");
+  MOE_REQUIRE(dgate == nullptr || (idx && gate), "dgate needs idx and gate");
+  MOE_REQUIRE(aligned(logits, 4) && aligned(idx, 4) && aligned(gate, 4) && aligned(dgate, 4) && aligned(counts, 4) &&
+                  aligned(coef, 4) && aligned(dloss, 4) && aligned(dlogits, 4), "misaligned pointer");
+  DeviceInfo dev;
+  st = current_device(&dev);
+  if (st != MOE_OK) return st;
+  const int blocks = (T + kWarps - 1) / kWarps;
+  const cudaError_t err = with_vpl(E, [&](auto vpl) {
+    router_backward_kernel<decltype(vpl)::value><<<blocks, kThreads, 0, stream>>>(
+        logits, T, E, idx, gate, dgate, k, seq_offsets, S, mask, counts, coef, dloss, dlogits, dev_status);
+    return cudaGetLastError();
+  });
+  if (err != cudaSuccess) return fail(MOE_ERR_CUDA, "router_backward launch: %s", cudaGetErrorString(err));
+  return MOE_OK;
+}

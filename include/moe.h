@@ -429,6 +429,101 @@ moe_status moe_profile_bandwidth(moe_shape s, const void* host_pool, int n_blobs
                                  double* host_gbs);
 
 /* ------------------------------------------------------------------------ */
+/* Dense 4-bit linear: y = x W^T with a weight matrix of 4-bit codes and one
+ * scale per group of consecutive K elements -- the dense parts that stand
+ * beside the routed experts (a shared expert, a projection, an output head).
+ * The pages have no counterpart to this call.
+ *   s:       W is [N][K]; 1 <= N <= 1 << 24, K a multiple of 32, K <= 1 << 17.
+ *     fmt MOE_W_MXFP4: E2M1 codes, E8M0 scales per 32 (byte 255 is NaN).
+ *     fmt MOE_W_NVFP4: E2M1 codes, E4M3 scales per 16, times tensor_scale.
+ *     fmt MOE_W_INT4:  w = scale * (code - zero), code in 0..15, group 32, 64
+ *                      or 128 (the last group of a row may be short), scales
+ *                      of type scale_type, zeros 0..15 (the low four bits are
+ *                      used) or NULL for 8 everywhere.
+ *     group is 32 for MXFP4 and 16 for NVFP4; scale_type counts for INT4 only.
+ *   codes:   device [N][K/2] bytes, element 2i in the low nibble.
+ *   scales:  device [N][ceil(K/group)]; zeros: device uint8 of that shape.
+ *   x:       device [T] rows of K elements, x_type MOE_DT_BF16 or MOE_DT_F16,
+ *            ldx elements apart (>= K, a multiple of 8).
+ *   y:       device [T] rows, ldy elements apart, y_type MOE_DT_F32 or x_type.
+ *            N elements a row; with MOE_LINEAR_SWIGLU N is even, rows 0..N/2-1
+ *            of W give h and rows N/2..N-1 give u, and a row of y is the N/2
+ *            values silu(h) * u.  With MOE_LINEAR_ACCUMULATE y += instead.
+ *            Elements of y outside these rows are left as they were; y may not
+ *            overlap x or the weights.
+ * Products are exact, sums are fp32 in a fixed order (the same call gives the
+ * same bits), y is rounded once.  x, scales, codes and y: codes and x 16-byte
+ * aligned, y and scales aligned to their element.  T >= 0 (T = 0 enqueues
+ * nothing), T <= 1 << 20. */
+typedef enum moe_dtype { MOE_DT_F32 = 0, MOE_DT_BF16 = 1, MOE_DT_F16 = 2 } moe_dtype;
+enum { MOE_W_INT4 = 3 };   /* moe_linear_shape.fmt only: experts have no INT4 blobs */
+enum { MOE_LINEAR_SWIGLU = 1, MOE_LINEAR_ACCUMULATE = 2 };
+typedef struct moe_linear_shape { int32_t N, K, fmt, group, scale_type; } moe_linear_shape;
+moe_status moe_linear_w4(moe_linear_shape s, const void* codes, const void* scales, const uint8_t* zeros,
+                         float tensor_scale, const void* x, int x_type, int64_t ldx, int T, void* y,
+                         int y_type, int64_t ldy, int flags, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Balance loss and per-expert counts of a routing, and the router's gradient.
+ * The pages leave the router unmodified; these calls are for a user who tunes
+ * or watches it while the experts stay as they are.
+ *   The batch is S sequences: sequence s holds the tokens seq_offsets[s] ..
+ *   seq_offsets[s+1]-1 (device int32 [S+1], nondecreasing, within [0, T]); NULL
+ *   with S = 1: all T tokens.  A token with mask[t] == 0 (device bytes [T], NULL:
+ *   none) or in no sequence is not part of the batch: its logits are never read.
+ *   With n_s tokens in sequence s, S' sequences that have tokens, n = sum n_s,
+ *   p_t = softmax(logits_t) over all E experts and lse_t its logsumexp:
+ *     counts[s][e] = pairs (t, j) of sequence s with idx[t][j] = e   (int32 [S][E])
+ *     prob[s][e]   = 1/n_s sum_t p_t[e], 0 if n_s = 0                (fp32 [S][E])
+ *     coef[s]      = E / (k n_s^2 S'), 0 if n_s = 0; coef[S] = 1/max(n, 1)
+ *     loss[0] = 1/S' sum_s E/(k n_s) sum_e counts[s][e] prob[s][e]
+ *             (1 for a uniform routing; 0 if S' = 0)
+ *     loss[1] = 1/n sum_t lse_t^2   (the router's z-loss; 0 if n = 0)
+ *   loss fp32 [2]; coef fp32 [S+1], read by the gradient.  Sums over tokens have a
+ *   fixed order, so the same call gives the same bits.
+ *   logits: device fp32 [T][E], finite or -inf (an expert that cannot be chosen:
+ *     p = 0); a row of nothing but -inf has p = 0 everywhere and adds nothing to
+ *     loss[1], while its token and pairs are counted.
+ *   idx: device int32 [T][k] (moe_route_topk's); an id outside [0, E) is recorded in
+ *     dev_status (device word or NULL) as MOE_ERR_DEVICE and its pair dropped, and so
+ *     are offsets that decrease or leave [0, T] (the results are then undefined).
+ *   workspace: device, 16-byte aligned, >= moe_balance_loss_workspace_bytes(T, E, S)
+ *     bytes, contents need no set-up; calls that overlap need one each.
+ * Limits as moe_route_topk; 1 <= S <= 1 << 20, 0 for arguments outside them. */
+size_t moe_balance_loss_workspace_bytes(int T, int E, int S);
+moe_status moe_balance_loss(const float* logits, int T, int E, const int32_t* idx, int k,
+                            const int32_t* seq_offsets, int S, const uint8_t* mask, float* loss,
+                            int32_t* counts, float* prob, float* coef, void* workspace, size_t ws_bytes,
+                            int32_t* dev_status, cudaStream_t stream);
+
+/* Gradient of the gates and of the two losses with respect to the logits, in one
+ * pass; counts are constants (they have no gradient):
+ *   dlogits[t][e] = dloss[0] coef[s] p_t[e] (counts[s][e] - sum_e' counts[s][e'] p_t[e'])
+ *                 + dloss[1] 2 coef[S] lse_t p_t[e]
+ *                 + sum_{j: idx[t][j] = e} gate[t][j] (dgate[t][j] - sum_i gate[t][i] dgate[t][i])
+ *   and 0 for a token that is not part of the batch.
+ *   dloss: device fp32 [2], or NULL: no loss terms (counts and coef are not read).
+ *   dgate: device fp32 [T][k], or NULL: no gate term (gate is not read); idx, gate:
+ *   moe_route_topk's.  counts, coef, seq_offsets, S, mask, logits: as above.
+ *   dlogits: device fp32 [T][E], overwritten. */
+moe_status moe_router_backward(const float* logits, int T, int E, const int32_t* idx, const float* gate,
+                               const float* dgate, int k, const int32_t* seq_offsets, int S,
+                               const uint8_t* mask, const int32_t* counts, const float* coef,
+                               const float* dloss, float* dlogits, int32_t* dev_status,
+                               cudaStream_t stream);
+
+/* Gradient of moe_combine_merge: for each pair p = t*k + j whose term the combine
+ * adds (same rules on slot_of_expert and inv_perm), with q = inv_perm[p],
+ *   dgate[t][j] = sum_c dout[t][c] y_perm[q][c]      dy_perm[q][c] = gate[t][j] dout[t][c]
+ * and dgate[t][j] = 0 for the others, whose rows of dy_perm are left as they were.
+ * (The gradient of host_partial is dout itself.)  dout fp32 [T][d]; dgate fp32
+ * [T][k]; dy_perm fp32 [T*k][d] or NULL (not wanted; gate is then not read). */
+moe_status moe_combine_backward(const float* y_perm, const int32_t* idx, const float* gate,
+                                const int32_t* inv_perm, const int32_t* slot_of_expert, const float* dout,
+                                int T, int k, int d, int E, float* dgate, float* dy_perm,
+                                cudaStream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* Synchronises `stream`, reads the device status word written by kernels,
  * resets it to 0 and returns it as a moe_status (MOE_OK if it was 0). */
 moe_status moe_check_status(int32_t* dev_status, cudaStream_t stream);

@@ -1,0 +1,316 @@
+"""moe_balance_loss, moe_router_backward and moe_combine_backward against the
+float64 oracle, at the sizes and masks where they can go wrong.
+
+Tolerances.  A probability is an fp32 exponential of a difference (each within a
+few steps of 2^-24) over a sum of E of them in log2(32) + E/32 adds: within
+(E/32 + 16) 2^-23 of its value, plus |logit - max| 2^-24 for the rounded
+difference (logits here stay below 16 apart: 2^-20 covers it).  Averages over
+tokens add at most n/8/592 + 8 fp32 steps more before the 64-bit sum.  Below:
+P = (E/32 + 48) 2^-23 for probabilities, means, lse^2 and the losses; a gradient
+is a product of such a probability with a difference of like terms, bounded by P
+times the sum of the terms' magnitudes."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import moe as M
+from oracle import router as R
+from tests.gpu_util import load_moe, require_gpu
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def moe():
+    require_gpu()
+    return load_moe()
+
+
+def routing(T, E, k, seed=0):
+    rng = np.random.default_rng(seed * 7919 + T * 31 + E)
+    l = (rng.standard_normal((T, E)) + 0.5 * rng.standard_normal(E)).astype(np.float32)
+    idx, gate = M.route_topk(l, k)
+    return rng, l, idx, gate.astype(np.float32)
+
+
+def dev(a, dt=None):
+    return None if a is None else torch.from_numpy(np.ascontiguousarray(a)).to("cuda", dt)
+
+
+def run_balance(moe, l, idx, off=None, mask=None, status=None, ws=None, **kw):
+    T, E = l.shape
+    S = 1 if off is None else len(off) - 1
+    o = dict(loss=torch.full((2,), -7.0, device="cuda"), counts=torch.full((S, E), -7, dtype=torch.int32, device="cuda"),
+             prob=torch.full((S, E), -7.0, device="cuda"), coef=torch.full((S + 1,), -7.0, device="cuda"))
+    if ws is None:
+        ws = torch.full((moe.moe_balance_loss_workspace_bytes(T, E, S),), 255, dtype=torch.uint8, device="cuda")
+    moe.moe_balance_loss(dev(l), dev(idx), o["loss"], o["counts"], o["prob"], o["coef"], ws,
+                         seq_offsets=None if off is None else dev(np.asarray(off, dtype=np.int32)),
+                         mask=None if mask is None else dev(np.asarray(mask, dtype=bool)), dev_status=status, **kw)
+    return o
+
+
+def check_balance(o, l, idx, off=None, mask=None):
+    E = l.shape[1]
+    P = (E / 32 + 48) * 2.0 ** -23
+    loss, counts, prob, coef = R.balance(l, idx, off, mask)
+    assert np.array_equal(o["counts"].cpu().numpy(), counts)
+    assert (np.abs(o["prob"].double().cpu().numpy() - prob) <= P * prob + 2.0 ** -126).all()
+    assert (np.abs(o["coef"].double().cpu().numpy() - coef) <= 2.0 ** -23 * coef).all()
+    assert (np.abs(o["loss"].double().cpu().numpy() - loss) <= P * np.abs(loss)).all(), (o["loss"], loss)
+
+
+SIZES = [(1, 1, 1), (1, 8, 2), (7, 33, 4), (64, 128, 8), (65, 64, 3), (200, 256, 6), (33, 512, 8), (19, 1000, 32),
+         (5, 1024, 1), (3000, 60, 5)]
+
+
+@pytest.mark.parametrize("T,E,k", SIZES)
+def test_balance_one_sequence(moe, T, E, k):
+    _, l, idx, _ = routing(T, E, k)
+    check_balance(run_balance(moe, l, idx), l, idx)
+
+
+@pytest.mark.parametrize("T,E,k", SIZES)
+def test_balance_sequences_and_mask(moe, T, E, k):
+    """Ragged sequences, empty ones, tokens before the first and behind the last,
+    masked tokens whose logits are NaN, a sequence with nothing left."""
+    rng, l, idx, _ = routing(T, E, k, 1)
+    cuts = np.sort(rng.integers(0, T + 1, 9))
+    off = np.concatenate([cuts[:3], cuts[2:3], cuts[2:]])
+    mask = rng.random(T) < 0.8
+    mask[off[4]:off[5]] = False
+    l[~mask] = np.nan
+    check_balance(run_balance(moe, l, idx, off, mask), l, idx, off, mask)
+
+
+def test_balance_many_short_sequences(moe):
+    T = 5000
+    _, l, idx, _ = routing(T, 40, 2, 2)
+    off = np.arange(T + 1)
+    check_balance(run_balance(moe, l, idx, off), l, idx, off)
+    check_balance(run_balance(moe, l, idx, off[::-1][:1].tolist() * 2000 + [T]), l, idx, [T] * 2001)
+
+
+def test_balance_nothing_left(moe):
+    _, l, idx, _ = routing(6, 16, 2, 3)
+    check_balance(run_balance(moe, l, idx, None, np.zeros(6, dtype=bool)), l, idx, None, np.zeros(6, dtype=bool))
+    o = run_balance(moe, l[:0], idx[:0])
+    assert o["loss"].tolist() == [0, 0] and (o["counts"] == 0).all() and (o["prob"] == 0).all()
+    assert o["coef"].tolist() == [0, 1]
+
+
+def test_balance_infinite_and_lowest_logits(moe):
+    """-inf switches an expert off; the type's lowest value is a number; a row of
+    -inf has no probabilities."""
+    _, l, idx, _ = routing(40, 70, 4, 4)
+    l[:, 5] = -np.inf
+    l[3] = -np.inf
+    l[4, 10:] = -np.inf
+    l[6, :60] = np.finfo(np.float32).min
+    l[7] = -80.0
+    for T in (40, 4):
+        check_balance(run_balance(moe, l[:T], idx[:T]), l[:T], idx[:T])
+
+
+def test_bad_ids_and_offsets_are_recorded(moe):
+    _, l, idx, _ = routing(50, 20, 3, 5)
+    bad = idx.copy()
+    bad[7, 1], bad[9, 0] = 20, -3
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    check_balance(run_balance(moe, l, bad, status=st), l, bad)
+    with pytest.raises(moe.MoeError) as e:
+        moe.moe_check_status(st)
+    assert e.value.status == moe.MOE_ERR_DEVICE
+    for off in ([0, 30, 20, 50], [-1, 10], [0, 51], [40, 10]):
+        run_balance(moe, l, idx, off, status=st)
+        with pytest.raises(moe.MoeError):
+            moe.moe_check_status(st)
+        dl = torch.zeros((50, 20), device="cuda")
+        S = len(off) - 1
+        moe.moe_router_backward(dev(l), dev(idx), dl, counts=torch.zeros((S, 20), dtype=torch.int32, device="cuda"),
+                                coef=torch.zeros(S + 1, device="cuda"), dloss=torch.ones(2, device="cuda"),
+                                seq_offsets=dev(np.asarray(off, dtype=np.int32)))
+    torch.cuda.synchronize()
+
+
+def run_router(moe, l, idx, gate=None, dgate=None, counts=None, coef=None, dloss=None, off=None, mask=None, **kw):
+    out = torch.full(l.shape, -7.0, device="cuda")
+    f = lambda a: None if a is None else dev(a, torch.float32)
+    moe.moe_router_backward(dev(l), dev(idx), out, gate=f(gate), dgate=f(dgate),
+                            counts=None if counts is None else dev(counts, torch.int32), coef=f(coef), dloss=f(dloss),
+                            seq_offsets=None if off is None else dev(np.asarray(off, dtype=np.int32)),
+                            mask=None if mask is None else dev(np.asarray(mask, dtype=np.uint8)), **kw)
+    return out
+
+
+def check_router(out, l, idx, gate, dgate, counts, coef, dloss, off, mask):
+    T, E = l.shape
+    P = (E / 32 + 48) * 2.0 ** -23
+    ref = R.router_backward(l, idx, gate, dgate, counts, coef, dloss, off, mask)
+    size = np.zeros((T, E))
+    for s, ts in enumerate(R.tokens_of(T, off, mask)):
+        if dloss is not None and ts:
+            p, lse = R.softmax_rows(l[ts])
+            c = np.asarray(counts[s], dtype=np.float64)
+            size[ts] += p * (abs(dloss[0]) * coef[s] * (c + (c * p).sum(1, keepdims=True))
+                             + 2 * abs(dloss[1]) * coef[-1] * np.abs(lse)[:, None])
+        if dgate is not None:
+            for t in ts:
+                for j, e in enumerate(idx[t]):
+                    if 0 <= e < E:
+                        size[t, e] += gate[t, j] * (abs(dgate[t, j]) + (gate[t] * np.abs(dgate[t])).sum())
+    assert (np.abs(out.double().cpu().numpy() - ref) <= P * size + 2.0 ** -126).all()
+
+
+@pytest.mark.parametrize("T,E,k", SIZES)
+@pytest.mark.parametrize("parts", ["both", "gates", "loss"])
+def test_router_backward(moe, T, E, k, parts):
+    rng, l, idx, gate = routing(T, E, k, 6)
+    for ragged in (False, True):
+        off = mask = None
+        if ragged:
+            off = np.sort(rng.integers(0, T + 1, 6))
+            mask = rng.random(T) < 0.8
+            l[~mask] = np.nan
+            gate[~mask] = np.nan
+        _, counts, _, coef = R.balance(l, idx, off, mask)
+        a = dict(counts=counts, coef=coef, dloss=np.array([0.6, -0.2], dtype=np.float32)) if parts != "gates" else \
+            dict(counts=None, coef=None, dloss=None)
+        a.update(dict(gate=gate, dgate=rng.standard_normal((T, k)).astype(np.float32)) if parts != "loss" else
+                 dict(gate=None, dgate=None))
+        if a["coef"] is not None:
+            a["coef"] = a["coef"].astype(np.float32)
+        out = run_router(moe, l, idx, off=off, mask=mask, **a)
+        check_router(out, l, idx, a["gate"], a["dgate"], a["counts"], a["coef"], a["dloss"], off, mask)
+
+
+def test_router_backward_infinite_logits_and_bad_ids(moe):
+    rng, l, idx, gate = routing(30, 50, 4, 7)
+    l[:, 11] = -np.inf
+    l[3] = -np.inf
+    idx[5, 2] = 50
+    idx[6, 0] = -1
+    _, counts, _, coef = R.balance(l, idx)
+    coef = coef.astype(np.float32)
+    dg = rng.standard_normal((30, 4)).astype(np.float32)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = run_router(moe, l, idx, gate, dg, counts, coef, np.array([1, 1], dtype=np.float32), dev_status=st)
+    check_router(out, l, idx, gate, dg, counts, coef, [1.0, 1.0], None, None)
+    with pytest.raises(moe.MoeError):
+        moe.moe_check_status(st)
+
+
+def test_gradient_against_differences_of_the_loss(moe):
+    """The forward's own loss, moved along a direction, changes by <dlogits, v>.
+    The loss is fp32 (a step is 2^-24 of ~6) and h = 2^-5 leaves h^2/6 f''' of the
+    third derivative, each far below 2e-3 of the change's size."""
+    rng, l, idx, _ = routing(24, 16, 2, 8)
+    off = [0, 10, 24]
+    o = run_balance(moe, l, idx, off)
+    d = run_router(moe, l, idx, counts=o["counts"].cpu().numpy(), coef=o["coef"].cpu().numpy(),
+                   dloss=np.array([1.0, 0.5], dtype=np.float32), off=off)
+    v = np.sign(d.cpu().numpy()).astype(np.float32)
+    f = lambda a: float((run_balance(moe, a.astype(np.float32), idx, off)["loss"].double().cpu() *
+                         torch.tensor([1.0, 0.5])).sum())
+    h = 2.0 ** -5
+    got = (f(l + h * v) - f(l - h * v)) / (2 * h)
+    want = float((d.double().cpu().numpy() * v).sum())
+    assert abs(got - want) <= 2e-3 * abs(want)
+
+
+@pytest.mark.parametrize("T,k,d,E", [(1, 1, 4, 1), (1, 8, 2048, 128), (5, 3, 260, 16), (17, 9, 1028, 40), (64, 8, 512, 128),
+                                     (3, 32, 64, 1024), (300, 6, 36, 256), (2, 2, 16384, 8)])
+def test_combine_backward(moe, T, k, d, E):
+    """dgate is an fp32 sum of d products: (d/1024 + 16) 2^-23 of the sum of their
+    magnitudes; dy is one product: half a step."""
+    rng, _, idx, gate = routing(T, E, k, 9)
+    _, _, inv = M.permute(idx, E)
+    y, dout = (rng.standard_normal(s).astype(np.float32) for s in ((T * k, d), (T, d)))
+    slot = np.where(rng.random(E) < 0.3, -1, np.arange(E)).astype(np.int32)
+    for sl in (slot, None):
+        for want_dy in (True, False):
+            y2 = y.copy()
+            if sl is not None:                              # rows that no term reads may hold anything
+                for p_, e in enumerate(idx.ravel()):
+                    if sl[e] < 0:
+                        y2[inv[p_]] = np.nan
+            dg = torch.full((T, k), -7.0, device="cuda")
+            dy = torch.full((T * k, d), -7.0, device="cuda") if want_dy else None
+            moe.moe_combine_backward(dev(y2), dev(idx), dev(gate), dev(inv), dev(sl), dev(dout), E, dg, dy_perm=dy)
+            rg, rdy = R.combine_backward(y2, idx, gate, inv, sl, dout, np.full((T * k, d), -7.0))
+            size = R.combine_backward(np.abs(y2), idx, gate, inv, sl, np.abs(dout), np.zeros((T * k, d)))[0]
+            assert (np.abs(dg.double().cpu().numpy() - rg) <= (d / 1024 + 16) * 2.0 ** -23 * size).all()
+            if want_dy:
+                assert (np.abs(dy.double().cpu().numpy() - rdy) <= 2.0 ** -24 * np.abs(rdy)).all()
+
+
+def test_combine_backward_bad_indices(moe):
+    """inv_perm or an id out of range drops the pair, as the combine does."""
+    rng, _, idx, gate = routing(6, 8, 2, 10)
+    _, _, inv = M.permute(idx, 8)
+    y, dout = (rng.standard_normal(s).astype(np.float32) for s in ((12, 16), (6, 16)))
+    inv, idx = inv.copy(), idx.copy()
+    inv[3], inv[4], idx[0, 1] = 12, -1, 9
+    slot = np.arange(8, dtype=np.int32)
+    dg = torch.full((6, 2), -7.0, device="cuda")
+    dy = torch.full((12, 16), -7.0, device="cuda")
+    moe.moe_combine_backward(dev(y), dev(idx), dev(gate), dev(inv), dev(slot), dev(dout), 8, dg, dy_perm=dy)
+    rg, rdy = R.combine_backward(y, idx, gate, inv, slot, dout, np.full((12, 16), -7.0))
+    assert np.allclose(dg.cpu().numpy(), rg, atol=1e-5) and np.allclose(dy.cpu().numpy(), rdy, atol=1e-6)
+
+
+def test_same_bits_graphs_and_streams(moe):
+    """Two eager calls, a call on another stream and a replayed graph (forward and
+    gradient in one) agree bit for bit."""
+    _, l, idx, gate = routing(900, 100, 4, 11)
+    off = [0, 100, 555, 900]
+    L, I, G = dev(l), dev(idx), dev(gate)
+    offs = dev(np.asarray(off, dtype=np.int32))
+    dgate = torch.randn((900, 4), device="cuda")
+    dloss = torch.tensor([0.5, 0.1], device="cuda")
+
+    def step(stream=None):
+        o = [torch.empty(2, device="cuda"), torch.empty((3, 100), dtype=torch.int32, device="cuda"),
+             torch.empty((3, 100), device="cuda"), torch.empty(4, device="cuda"), torch.empty((900, 100), device="cuda")]
+        ws = torch.empty(moe.moe_balance_loss_workspace_bytes(900, 100, 3), dtype=torch.uint8, device="cuda")
+        moe.moe_balance_loss(L, I, *o[:4], ws, seq_offsets=offs, stream=stream)
+        moe.moe_router_backward(L, I, o[4], gate=G, dgate=dgate, counts=o[1], coef=o[3], dloss=dloss, seq_offsets=offs,
+                                stream=stream)
+        return o + [ws]
+    first, second = step(), step()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    third = step(side)
+    side.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        fourth = step()
+    for _ in range(2):
+        for t in fourth[:5]:
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        for other in (second, third, fourth):
+            for a, b in zip(first[:5], other[:5]):
+                assert torch.equal(a, b)
+
+
+def test_binding_refusals(moe):
+    l, i = torch.zeros((4, 8), device="cuda"), torch.zeros((4, 2), dtype=torch.int32, device="cuda")
+    o = [torch.empty(2, device="cuda"), torch.empty((1, 8), dtype=torch.int32, device="cuda"),
+         torch.empty((1, 8), device="cuda"), torch.empty(2, device="cuda")]
+    ws = torch.empty(moe.moe_balance_loss_workspace_bytes(4, 8, 1), dtype=torch.uint8, device="cuda")
+    with pytest.raises(ValueError):
+        moe.moe_balance_loss(l.half(), i, *o, ws)
+    with pytest.raises(ValueError):
+        moe.moe_balance_loss(l, i, *o, ws, seq_offsets=torch.zeros(3, dtype=torch.int32, device="cuda"))   # S = 2
+    with pytest.raises(ValueError):
+        moe.moe_balance_loss(l, i, *o, ws, mask=torch.ones(3, dtype=torch.bool, device="cuda"))
+    with pytest.raises(moe.MoeError):
+        moe.moe_balance_loss(l, i, *o, ws[:64])
+    with pytest.raises(ValueError):
+        moe.moe_router_backward(l, i, l[:3])
+    with pytest.raises(moe.MoeError):
+        moe.moe_router_backward(l, i, l.clone(), dgate=torch.zeros((4, 2), device="cuda"))
+    with pytest.raises(ValueError):
+        moe.moe_combine_backward(l, i, o[2], i, None, l, 8, o[2])
