@@ -290,22 +290,56 @@ def moe_layer_forward(s: moe_shape, logits, x, k: int, idx, gate, offsets, perm,
                                    _ptr(out), _ptr(dev_status), _stream(stream)))
 
 
-def _here(*tensors):
-    """The calls below run on the current device: their tensors must live there."""
-    cur = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != cur:
-            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{cur}")
+# The calls below are short kernels, so the host's share of a call counts: every
+# tensor is checked and resolved to its address in one pass (_mem), on the
+# current device, and the stream is taken without building a torch.cuda.Stream.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _rows(name, t, n, width):
-    """A CUDA matrix of n rows of `width` elements, any distance apart; returns it."""
-    if not t.is_cuda or t.dim() != 2 or t.shape[0] != n or t.shape[1] != width or (width > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name}: expected a CUDA [{n}, {width}] tensor with contiguous rows, got {t.dtype} "
-                         f"{tuple(t.shape)} with strides {t.stride()} on {t.device}")
-    if n > 1 and t.stride(0) < width:
-        raise ValueError(f"{name}: rows overlap (stride {t.stride(0)} < {width})")
-    return t.stride(0) if n > 1 else max(t.stride(0), width)
+def _mem(name, t, n, dtype, dev):
+    """Address of a contiguous tensor on CUDA device `dev` of the documented
+    dtype with the n elements the call touches; None for None."""
+    if t is None:
+        return None
+    if t.get_device() != dev or t.dtype is not dtype or t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of >= {n} elements on the current device "
+                         f"cuda:{dev}, got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
+    return t.data_ptr()
+
+
+def _matrix(name, t, rows, cols, dtype, dev):
+    """_mem of a tensor of exactly [rows, cols]."""
+    if t is None:
+        return None
+    if t.shape != (rows, cols) or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {(rows, cols)} on the current device "
+                         f"cuda:{dev}, got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
+    return t.data_ptr()
+
+
+def _rows(name, t, shape, dev):
+    """Row distance of a matrix of `shape` on the device whose rows are
+    contiguous and do not overlap."""
+    st = t.stride()
+    n, width = shape
+    if t.get_device() != dev or t.shape != shape or (st[1] != 1 and width > 1) or (st[0] < width and n > 1):
+        raise ValueError(f"{name}: expected a {tuple(shape)} tensor with contiguous rows on the current device "
+                         f"cuda:{dev}, got {t.dtype} {tuple(t.shape)} with strides {st} on {t.device}")
+    return st[0] if n > 1 else (width + 7) // 8 * 8       # a single row has no distance
+
+
+def _device_of(name, t):
+    """The current device, which has to be the one that t is on."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}: expected the current CUDA device")
+    return dev
+
+
+def _current(stream, dev):
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(dev)
+    return _stream(stream)
 
 
 def moe_linear_w4(x, codes, scales, out, fmt="int4", group: int = 128, zeros=None, tensor_scale: float = 1.0,
@@ -316,41 +350,40 @@ def moe_linear_w4(x, codes, scales, out, fmt="int4", group: int = 128, zeros=Non
     "nvfp4" (scales uint8, group 32 or 16).  x [T, K] bf16 or fp16, out [T, N] of
     x's type or fp32; rows of both may be any distance apart.  swiglu: out
     [T, N/2] = silu(h) * u of W's two row halves."""
+    f = LINEAR_FORMATS[fmt]
+    dev = _device_of("x", x)
     T, K = x.shape
     N = codes.shape[0]
-    f = LINEAR_FORMATS[fmt]
+    if group <= 0:
+        raise ValueError(f"group={group}")
     G = -(-K // group)
-    _dev("codes", codes, N * (K // 2), torch.uint8)
-    _dev("scales", scales, N * G, torch.uint8 if f != MOE_W_INT4 else scales.dtype)
-    _dev("zeros", zeros, N * G, torch.uint8)
-    for name, t, want in (("codes", codes, (N, K // 2)), ("scales", scales, (N, G)), ("zeros", zeros, (N, G))):
-        if t is not None and tuple(t.shape) != want:
-            raise ValueError(f"{name}: expected shape {want} for K={K}, group={group}, got {tuple(t.shape)}")
-    if f == MOE_W_INT4 and scales.dtype not in DTYPES:
-        raise ValueError(f"scales: expected float32, bfloat16 or float16, got {scales.dtype}")
+    sdt = scales.dtype
+    if f == MOE_W_INT4 and sdt not in DTYPES:
+        raise ValueError(f"scales: expected float32, bfloat16 or float16, got {sdt}")
     if x.dtype not in DTYPES or out.dtype not in DTYPES:
         raise ValueError(f"x {x.dtype}, out {out.dtype}: expected bfloat16 or float16, and that or float32")
-    ldx, ldy = _rows("x", x, T, K), _rows("out", out, T, N // 2 if swiglu else N)
-    _here(x, codes, scales, zeros, out)
-    s = moe_linear_shape(N, K, f, group, DTYPES.get(scales.dtype, MOE_DT_F32))
-    if T == 1:
-        ldx = (ldx + 7) // 8 * 8          # the distance of rows that are not there
-    _check(lib().moe_linear_w4(s, _ptr(codes), _ptr(scales), _ptr(zeros), tensor_scale, _ptr(x), DTYPES[x.dtype], ldx,
-                               T, _ptr(out), DTYPES[out.dtype], ldy,
-                               (MOE_LINEAR_SWIGLU if swiglu else 0) | (MOE_LINEAR_ACCUMULATE if accumulate else 0),
-                               _stream(stream)))
+    pc = _matrix("codes", codes, N, K // 2, torch.uint8, dev)
+    ps = _matrix("scales", scales, N, G, sdt if f == MOE_W_INT4 else torch.uint8, dev)
+    pz = _matrix("zeros", zeros, N, G, torch.uint8, dev)
+    ldx, ldy = _rows("x", x, (T, K), dev), _rows("out", out, (T, N // 2 if swiglu else N), dev)
+    st = (_lib or lib()).moe_linear_w4(
+        moe_linear_shape(N, K, f, group, DTYPES.get(sdt, MOE_DT_F32)), pc, ps, pz, tensor_scale, x.data_ptr(),
+        DTYPES[x.dtype], ldx, T, out.data_ptr(), DTYPES[out.dtype], ldy,
+        (MOE_LINEAR_SWIGLU if swiglu else 0) | (MOE_LINEAR_ACCUMULATE if accumulate else 0), _current(stream, dev))
+    if st:
+        _check(st)
 
 
-def _batch(logits, idx, seq_offsets, mask):
+def _batch(logits, idx, seq_offsets, mask, dev):
+    """T, E, k, S and the addresses of a routed batch."""
     T, E = logits.shape
     k = idx.shape[1]
     S = 1 if seq_offsets is None else seq_offsets.numel() - 1
-    _dev("logits", logits, T * E, torch.float32)
-    _dev("idx", idx, T * k, torch.int32)
-    _dev("seq_offsets", seq_offsets, S + 1, torch.int32)
-    if mask is not None:
-        _dev("mask", mask, T, torch.bool if mask.dtype == torch.bool else torch.uint8)
-    return T, E, k, S
+    if mask is not None and mask.dtype is not torch.bool and mask.dtype is not torch.uint8:
+        raise ValueError(f"mask: expected bool or uint8, got {mask.dtype}")
+    return (T, E, k, S, _mem("logits", logits, T * E, torch.float32, dev),
+            _matrix("idx", idx, T, k, torch.int32, dev), _mem("seq_offsets", seq_offsets, S + 1, torch.int32, dev),
+            None if mask is None else _mem("mask", mask, T, mask.dtype, dev))
 
 
 def moe_balance_loss_workspace_bytes(T: int, E: int, S: int = 1) -> int:
@@ -362,54 +395,49 @@ def moe_balance_loss(logits, idx, loss, counts, prob, coef, workspace, seq_offse
     """loss [2] = (balance loss, z-loss), counts [S, E] int32, prob [S, E] and
     coef [S + 1] of the routing idx [T, k] of logits [T, E]; seq_offsets int32
     [S + 1] (None: one sequence), mask [T] bool or uint8 (None: every token)."""
-    T, E, k, S = _batch(logits, idx, seq_offsets, mask)
-    _dev("loss", loss, 2, torch.float32)
-    _dev("counts", counts, S * E, torch.int32)
-    _dev("prob", prob, S * E, torch.float32)
-    _dev("coef", coef, S + 1, torch.float32)
-    _dev("workspace", workspace, 0, torch.uint8)
-    _dev("dev_status", dev_status, 1, torch.int32)
-    _here(logits, idx, loss, counts, prob, coef, workspace, seq_offsets, mask, dev_status)
-    _check(lib().moe_balance_loss(_ptr(logits), T, E, _ptr(idx), k, _ptr(seq_offsets), S, _ptr(mask), _ptr(loss),
-                                  _ptr(counts), _ptr(prob), _ptr(coef), _ptr(workspace), workspace.numel(),
-                                  _ptr(dev_status), _stream(stream)))
+    dev = _device_of("logits", logits)
+    f32 = torch.float32
+    T, E, k, S, pl, pi, po, pm = _batch(logits, idx, seq_offsets, mask, dev)
+    st = (_lib or lib()).moe_balance_loss(
+        pl, T, E, pi, k, po, S, pm, _mem("loss", loss, 2, f32, dev), _mem("counts", counts, S * E, torch.int32, dev),
+        _mem("prob", prob, S * E, f32, dev), _mem("coef", coef, S + 1, f32, dev),
+        _mem("workspace", workspace, 0, torch.uint8, dev), workspace.numel(),
+        _mem("dev_status", dev_status, 1, torch.int32, dev), _current(stream, dev))
+    if st:
+        _check(st)
 
 
 def moe_router_backward(logits, idx, dlogits, gate=None, dgate=None, counts=None, coef=None, dloss=None,
                         seq_offsets=None, mask=None, dev_status=None, stream=None):
     """dlogits [T, E] of the gates (dgate [T, k]; None: no such term) and of the
     losses (dloss [2], with counts and coef of moe_balance_loss; None: none)."""
-    T, E, k, S = _batch(logits, idx, seq_offsets, mask)
-    _dev("dlogits", dlogits, T * E, torch.float32)
-    _dev("gate", gate, T * k, torch.float32)
-    _dev("dgate", dgate, T * k, torch.float32)
-    _dev("counts", counts, S * E, torch.int32)
-    _dev("coef", coef, S + 1, torch.float32)
-    _dev("dloss", dloss, 2, torch.float32)
-    _dev("dev_status", dev_status, 1, torch.int32)
-    _here(logits, idx, dlogits, gate, dgate, counts, coef, dloss, seq_offsets, mask, dev_status)
-    _check(lib().moe_router_backward(_ptr(logits), T, E, _ptr(idx), _ptr(gate), _ptr(dgate), k, _ptr(seq_offsets), S,
-                                     _ptr(mask), _ptr(counts), _ptr(coef), _ptr(dloss), _ptr(dlogits),
-                                     _ptr(dev_status), _stream(stream)))
+    dev = _device_of("logits", logits)
+    f32 = torch.float32
+    T, E, k, S, pl, pi, po, pm = _batch(logits, idx, seq_offsets, mask, dev)
+    st = (_lib or lib()).moe_router_backward(
+        pl, T, E, pi, _mem("gate", gate, T * k, f32, dev), _mem("dgate", dgate, T * k, f32, dev), k, po, S, pm,
+        _mem("counts", counts, S * E, torch.int32, dev), _mem("coef", coef, S + 1, f32, dev),
+        _mem("dloss", dloss, 2, f32, dev), _mem("dlogits", dlogits, T * E, f32, dev),
+        _mem("dev_status", dev_status, 1, torch.int32, dev), _current(stream, dev))
+    if st:
+        _check(st)
 
 
 def moe_combine_backward(y_perm, idx, gate, inv_perm, slot_of_expert, dout, E: int, dgate, dy_perm=None, stream=None):
     """dgate [T, k] and, if wanted, dy_perm [T*k, d] from dout [T, d], for the
     pairs moe_combine_merge adds (the other pairs' dgate is 0, their dy_perm
     rows stay as they are)."""
+    dev = _device_of("dout", dout)
+    f32, i32 = torch.float32, torch.int32
     T, k = idx.shape
-    d = dout.shape[1]
-    _dev("y_perm", y_perm, T * k * d, torch.float32)
-    _dev("idx", idx, T * k, torch.int32)
-    _dev("gate", gate, T * k, torch.float32)
-    _dev("inv_perm", inv_perm, T * k, torch.int32)
-    _dev("slot_of_expert", slot_of_expert, E, torch.int32)
-    _dev("dout", dout, T * d, torch.float32)
-    _dev("dgate", dgate, T * k, torch.float32)
-    _dev("dy_perm", dy_perm, T * k * d, torch.float32)
-    _here(y_perm, idx, gate, inv_perm, slot_of_expert, dout, dgate, dy_perm)
-    _check(lib().moe_combine_backward(_ptr(y_perm), _ptr(idx), _ptr(gate), _ptr(inv_perm), _ptr(slot_of_expert),
-                                      _ptr(dout), T, k, d, E, _ptr(dgate), _ptr(dy_perm), _stream(stream)))
+    n, d = T * k, dout.shape[1]
+    st = (_lib or lib()).moe_combine_backward(
+        _mem("y_perm", y_perm, n * d, f32, dev), _mem("idx", idx, n, i32, dev), _mem("gate", gate, n, f32, dev),
+        _mem("inv_perm", inv_perm, n, i32, dev), _mem("slot_of_expert", slot_of_expert, E, i32, dev),
+        _mem("dout", dout, T * d, f32, dev), T, k, d, E, _mem("dgate", dgate, n, f32, dev),
+        _mem("dy_perm", dy_perm, n * d, f32, dev), _current(stream, dev))
+    if st:
+        _check(st)
 
 
 def moe_split_misses(misses, tokens_per_expert, q=None, bw_pcie=0.0, bw_host=0.0):

@@ -1,0 +1,512 @@
+// Dense 4-bit linear: y[t][n] = sum_k w[n][k] x[t][k], w from 4-bit codes and a
+// scale per group of K.  The kernel, instantiated per format in linear_w4_*.cu.
+//
+// A CTA of 8 warps multiplies M rows of W by a tile of tokens with mma.sync
+// (m16n8k16, fp32 accumulators); a warp has 16 * RT rows, 8 * NT tokens and a
+// slice of K.  Codes and x arrive in stages of KS elements of K through a
+// cp.async ring that all warps share; scales (and zeros) are fetched two stages
+// ahead into registers, turned into what the product needs and put into shared
+// memory one stage ahead.  One CTA barrier a stage.
+//
+// A thread turns 8 codes of a row (one 32-bit word) into four operand pairs of
+// the x type, exactly:
+//   INT4   code - zero             an integer of at most 4 bits
+//   MXFP4  the E2M1 value          2 significant bits
+//   NVFP4  E2M1 * E4M3 block scale 6 significant bits
+// INT4 and MXFP4 scales multiply the fp32 sum of their group (or 32-element
+// block), so every product is exact and only fp32 sums round.
+//
+// K order.  The MMA's k slots may hold any 16 elements as long as both operands
+// agree.  A quad's four threads hold 8 consecutive k each, 32 in all: two MMAs.
+// INT4: masking the halves of a shifted word yields the pairs (k, k+4), ...,
+// (k+3, k+7); the words of x are permuted alike.  E2M1: a byte converts to the
+// pair (k, k+1), x as it is.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+
+namespace moe {
+
+struct LinearParams {
+  const uint8_t* codes;
+  const void* scales;
+  const uint8_t* zeros;
+  const void* x;
+  void* y;
+  int64_t ldx, ldy;
+  int N, K, T, groups, scale_type, y_f32, swiglu, accumulate;
+  float tensor_scale;
+  // launch shape
+  int wm_bits, wn_bits;    // warps along the rows and the tokens (log2); the other warps split K
+  int stages, ring;        // stages in flight + 1; slots (no more than there are stages)
+  int x_rows;              // token rows a stage holds
+};
+
+// Launchers, one per format family (linear_w4_int4.cu, linear_w4_fp4.cu).
+cudaError_t launch_linear_int4(const LinearParams& P, int group, bool bf16, const DeviceInfo& dev, cudaStream_t s);
+cudaError_t launch_linear_fp4(const LinearParams& P, int fmt, bool bf16, const DeviceInfo& dev, cudaStream_t s);
+
+namespace w4 {
+
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until at most n groups are in flight (n is the same for every thread).
+__device__ __forceinline__ void cp_wait(int n) {
+  switch (n) {
+    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+  }
+}
+constexpr int kMaxStages = 5;
+
+template <typename V>
+__device__ __forceinline__ V lds(const unsigned char* smem, uint32_t at) {
+  return *reinterpret_cast<const V*>(smem + at);
+}
+
+// c = a b (+ c)
+template <bool BF16, bool ZERO>
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+#define MOE_MMA(TYPE)                                                                                               \
+  if constexpr (ZERO)                                                                                               \
+    asm("mma.sync.aligned.m16n8k16.row.col.f32." TYPE "." TYPE                                             \
+                 ".f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"                                   \
+                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])                                                   \
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));                                 \
+  else                                                                                                              \
+    asm("mma.sync.aligned.m16n8k16.row.col.f32." TYPE "." TYPE                                             \
+                 ".f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"                                       \
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])                                                   \
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  if constexpr (BF16) {
+    MOE_MMA("bf16")
+  } else {
+    MOE_MMA("f16")
+  }
+#undef MOE_MMA
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if constexpr (BF16) asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if constexpr (BF16) asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Pair I (0..3) of a word as two exact values of the x type.
+//   INT4: `c` holds (M + zero, M + zero) with M = 128 (bf16) or 1024 (f16), where
+//   the type's step is 1, and a code is OR-ed into M's low bits.
+//   E2M1: the conversion to f16; for bf16 the exponent and the top of the
+//   mantissa move 3 places down, which reads as the value * 2^-112; `c` takes
+//   that back, and multiplies with NVFP4's block scale.
+template <int FMT, bool BF16, int I>
+__device__ __forceinline__ uint32_t pair_of(uint32_t w, uint32_t c) {
+  if constexpr (FMT == MOE_W_INT4) {
+    constexpr uint32_t M = BF16 ? 0x43004300u : 0x64006400u;
+    return sub2<BF16>(((w >> (4 * I)) & 0x000F000Fu) | M, c);
+  } else {
+    uint32_t h;
+    asm("{ .reg .b8 b; cvt.u8.u32 b, %1; cvt.rn.f16x2.e2m1x2 %0, b; }" : "=r"(h) : "r"(w >> (8 * I)));
+    if constexpr (BF16) return mul2<true>((h & 0x80008000u) | ((h >> 3) & 0x0FFF0FFFu), c);
+    return FMT == MOE_W_NVFP4 ? mul2<false>(h, c) : h;
+  }
+}
+constexpr uint32_t kBf16Back = 0x77807780u;   // 2^112 twice
+
+// E8M0: 2^(b - 127); 0 is a subnormal of fp32, 255 is NaN.
+__device__ __forceinline__ float e8m0_value(uint32_t b) {
+  return __uint_as_float(b == 255 ? 0x7FC00000u : (b == 0 ? 0x00400000u : b << 23));
+}
+
+// E4M3 block scale as the multiplier `c` of pair_of (4 significant bits: exact).
+template <bool BF16>
+__device__ __forceinline__ uint32_t e4m3_mult(uint32_t b) {
+  const __half h = __half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(b), __NV_E4M3));
+  uint32_t u;
+  if constexpr (BF16) u = __float_as_uint(__half2float(h) * 5.192296858534828e33f) >> 16;   // * 2^112
+  else u = __half_as_ushort(h);
+  return u | (u << 16);
+}
+
+// Row of W that tile row r of the 16-row tile `tile` holds (clamped to the last
+// one): with SwiGLU rows 0-7 are gate rows and 8-15 the up rows of the same outputs.
+__device__ __forceinline__ int weight_row(const LinearParams& P, int tile, int r) {
+  if (P.swiglu) {
+    const int half = P.N >> 1, i = min(tile * 8 + (r & 7), half - 1);
+    return r < 8 ? i : half + i;
+  }
+  return min(tile * 16 + r, P.N - 1);
+}
+
+template <bool BF16>
+__device__ __forceinline__ void store_y(const LinearParams& P, int t, int n, float v) {
+  const int64_t at = static_cast<int64_t>(t) * P.ldy + n;
+  if (P.y_f32) {
+    float* y = static_cast<float*>(P.y) + at;
+    *y = P.accumulate ? *y + v : v;
+  } else if (BF16) {
+    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(P.y) + at;
+    *y = __float2bfloat16_rn(P.accumulate ? __bfloat162float(*y) + v : v);
+  } else {
+    __half* y = static_cast<__half*>(P.y) + at;
+    *y = __float2half_rn(P.accumulate ? __half2float(*y) + v : v);
+  }
+}
+
+// GROUP: elements of K per scale.  KW: elements of K a warp takes from a stage.
+template <int FMT, int GROUP, bool BF16, int NT, int RT>
+struct Geometry {
+  static constexpr int KW = RT == 1 ? 256 : 128;
+  static constexpr int STAGE_WEIGHTS = 8 * 16 * RT * KW;                // at one warp tile of tokens
+  static constexpr int EPT = STAGE_WEIGHTS / GROUP / kThreads;          // scales a thread fetches per stage
+  static constexpr int CPT = STAGE_WEIGHTS / 32 / kThreads;             // 16-byte chunks of codes a thread copies
+  static constexpr int ENTRY = FMT == MOE_W_INT4 ? 8 : 4;               // bytes of a scale in shared memory
+  int wk, ks, m, tokens, gps, cpitch, xpitch, spitch, stage, sbuf, zero_at, s_at, bytes;
+  // wk: warps along K; ks: K per stage; m: rows; gps: groups of a row per stage;
+  // pitches: bytes of a row of codes (conflict-free 4-byte reads of 8 rows), of x
+  // (16-byte reads of 2 rows) and of scales (odd in entries)
+  __host__ __device__ explicit Geometry(const LinearParams& P) {
+    wk = 8 >> P.wm_bits >> P.wn_bits;
+    ks = KW * wk;
+    m = 16 * RT << P.wm_bits;
+    tokens = 8 * NT << P.wn_bits;
+    gps = ks / GROUP;
+    cpitch = ks / 2 + 16;
+    xpitch = ks * 2 + 64;
+    spitch = (gps + 1) * ENTRY;
+    stage = m * cpitch + P.x_rows * xpitch;
+    sbuf = (m * spitch + 15) / 16 * 16;
+    zero_at = P.ring * stage;                 // one row of zeros for the tokens that are not there
+    s_at = zero_at + xpitch;
+    bytes = s_at + 2 * sbuf;
+  }
+};
+
+template <int FMT, int GROUP, bool BF16, int NT, int RT>
+__global__ void __launch_bounds__(kThreads, RT == 1 ? 2 : 1) linear_w4_kernel(const __grid_constant__ LinearParams P) {
+  using G = Geometry<FMT, GROUP, BF16, NT, RT>;
+  constexpr int KW = G::KW, KB = KW / 32, GB = GROUP >= 32 ? GROUP / 32 : 1;
+  extern __shared__ __align__(16) unsigned char smem[];
+  const G geo(P);
+  const uint32_t sm = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
+  const int wm = warp & ((1 << P.wm_bits) - 1), wn = (warp >> P.wm_bits) & ((1 << P.wn_bits) - 1);
+  const int wk = warp >> P.wm_bits >> P.wn_bits;
+  const int tile0 = blockIdx.x * (geo.m / 16);                       // first 16-row tile of the CTA
+  const int tok0 = blockIdx.y * geo.tokens;
+  const int x_rows = min(P.x_rows, P.T - tok0);
+  const int nst = (P.K + geo.ks - 1) / geo.ks;
+  pdl_wait();
+  pdl_trigger();
+
+  // A stage's copies: thread -> 16-byte chunk `col` of every code_rows-th row (a
+  // row of codes has a power of two <= 64 chunks, a row of x four times as many).
+  const int cpr_bits = 31 - __clz(geo.ks / 32), col = tid & ((1 << cpr_bits) - 1);
+  const int code_rows = kThreads >> cpr_bits, code_r = tid >> cpr_bits;
+  const uint8_t* src[G::CPT];
+#pragma unroll
+  for (int i = 0; i < G::CPT; ++i) {
+    const int r = min(i * code_rows + code_r, geo.m - 1);
+    src[i] = P.codes + static_cast<size_t>(weight_row(P, tile0 + (r >> 4), r & 15)) * (P.K >> 1) + col * 16;
+  }
+  const int xpr_bits = cpr_bits + 2, xcol = tid & ((1 << xpr_bits) - 1);
+  const int xrow_step = kThreads >> xpr_bits, xr0 = tid >> xpr_bits;
+  const uint16_t* xsrc = static_cast<const uint16_t*>(P.x) + static_cast<int64_t>(tok0 + xr0) * P.ldx + xcol * 8;
+  const int64_t xstep = xrow_step * P.ldx;
+  const uint32_t cdst = sm + code_r * geo.cpitch + col * 16;
+  const uint32_t xdst = sm + geo.m * geo.cpitch + xr0 * geo.xpitch + xcol * 16;
+  int slot_in = 0;                                                   // slot of the next stage to issue
+  auto issue = [&](int st) {
+    if (st < nst) {
+      const int k0 = st * geo.ks;
+      const uint32_t at = slot_in * geo.stage;
+      const bool ok = k0 + col * 32 < P.K;
+#pragma unroll
+      for (int i = 0; i < G::CPT; ++i)
+        if (i * code_rows + code_r < geo.m)
+          cp_async16(cdst + at + i * code_rows * geo.cpitch, ok ? src[i] + (k0 >> 1) : P.codes, ok);
+      const bool xok = k0 + xcol * 8 < P.K;
+      const uint16_t* xp = xsrc + k0;
+      uint32_t xd = xdst + at;
+      for (int r = xr0; r < x_rows; r += xrow_step) {
+        cp_async16(xd, xok ? static_cast<const void*>(xp) : P.x, xok);
+        xp += xstep;
+        xd += xrow_step * geo.xpitch;
+      }
+      slot_in = slot_in + 1 == P.ring ? 0 : slot_in + 1;
+    }
+    cp_commit();
+  };
+  for (int i = 0; i < P.stages - 1; ++i) issue(i);
+
+  // Scales of a stage: thread -> group `sg` of every s_rows-th row; raw values in registers.
+  const int gps_bits = 31 - __clz(geo.gps), sg = tid & (geo.gps - 1);
+  const int s_rows = kThreads >> gps_bits, s_r = tid >> gps_bits;
+  int srow[G::EPT];
+#pragma unroll
+  for (int i = 0; i < G::EPT; ++i) {
+    const int r = min(i * s_rows + s_r, geo.m - 1);
+    srow[i] = weight_row(P, tile0 + (r >> 4), r & 15);
+  }
+  uint32_t sraw[G::EPT], zraw[G::EPT];
+  auto fetch = [&](int st) {
+    const int j = st * geo.gps + sg;
+#pragma unroll
+    for (int i = 0; i < G::EPT; ++i) {
+      sraw[i] = 0;
+      zraw[i] = 8;
+      if (j < P.groups) {
+        const size_t at = static_cast<size_t>(static_cast<uint32_t>(srow[i])) * static_cast<uint32_t>(P.groups) + j;
+        if constexpr (FMT == MOE_W_INT4) {
+          sraw[i] = P.scale_type == MOE_DT_F32 ? __ldg(static_cast<const uint32_t*>(P.scales) + at)
+                                               : __ldg(static_cast<const uint16_t*>(P.scales) + at);
+          if (P.zeros != nullptr) zraw[i] = __ldg(P.zeros + at) & 15u;
+        } else {
+          sraw[i] = 0x100u | __ldg(static_cast<const uint8_t*>(P.scales) + at);   // 0x100: there is one
+        }
+      }
+    }
+  };
+  unsigned char* const sdst = smem + geo.s_at + s_r * geo.spitch + sg * G::ENTRY;
+  auto put = [&](int st) {
+    unsigned char* d = sdst + (st & 1) * geo.sbuf;
+#pragma unroll
+    for (int i = 0; i < G::EPT; ++i, d += s_rows * geo.spitch) {
+      if (i * s_rows + s_r >= geo.m) break;
+      if constexpr (FMT == MOE_W_INT4) {
+        const uint32_t f = P.scale_type == MOE_DT_F32    ? sraw[i]
+                           : P.scale_type == MOE_DT_BF16 ? sraw[i] << 16
+                                                         : __float_as_uint(__half2float(__ushort_as_half(sraw[i])));
+        *reinterpret_cast<uint2*>(d) = make_uint2(f, ((BF16 ? 0x4300u : 0x6400u) | zraw[i]) * 0x10001u);
+      } else if constexpr (FMT == MOE_W_MXFP4) {
+        *reinterpret_cast<float*>(d) = sraw[i] == 0 ? 0.f : e8m0_value(sraw[i] & 255u);
+      } else {
+        *reinterpret_cast<uint32_t*>(d) = sraw[i] == 0 ? 0u : e4m3_mult<BF16>(sraw[i] & 255u);
+      }
+    }
+  };
+  fetch(0);
+  for (int c = tid; c < geo.xpitch / 16; c += kThreads)
+    *reinterpret_cast<uint4*>(smem + geo.zero_at + c * 16) = make_uint4(0, 0, 0, 0);
+  put(0);
+  if (nst > 1) fetch(1);
+
+  float acc[RT][NT][4], part[RT][NT][4];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[rt][nt][i] = 0.f;
+
+  const int row = wm * 16 * RT + g;                                  // this thread's rows: row + 8 i
+  const uint32_t code_at = row * geo.cpitch + wk * (KW / 2) + t4 * 4;
+  const uint32_t scale_at = geo.s_at + row * geo.spitch +
+                            (wk * (KW / GROUP) + (FMT == MOE_W_NVFP4 ? t4 >> 1 : 0)) * G::ENTRY;
+  const uint32_t x_at = geo.m * geo.cpitch + (wn * 8 * NT + g) * geo.xpitch + wk * (KW * 2) + t4 * 16;
+  int slot = 0;
+  for (int st = 0; st < nst; ++st) {
+    cp_wait(P.stages - 2);
+    __syncthreads();
+    if (st + 1 < nst) put(st + 1);
+    if (st + 2 < nst) fetch(st + 2);
+    issue(st + P.stages - 1);
+    const uint32_t at = slot * geo.stage;
+    slot = slot + 1 == P.ring ? 0 : slot + 1;
+    if (st * geo.ks + wk * KW >= P.K) continue;                      // this warp's share lies behind K
+    const uint32_t ca = at + code_at, sa = scale_at + (st & 1) * geo.sbuf;
+    uint32_t xa[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+      xa[nt] = wn * 8 * NT + nt * 8 + g < x_rows ? at + x_at + nt * 8 * geo.xpitch : geo.zero_at + t4 * 16;
+    uint32_t c[2 * RT];
+    float f[2 * RT];
+#pragma unroll
+    for (int b = 0; b < KB; ++b) {
+      uint32_t a[RT][2][4];
+#pragma unroll
+      for (int i = 0; i < 2 * RT; ++i) {
+        const uint32_t so = sa + i * 8 * geo.spitch;
+        if constexpr (FMT == MOE_W_INT4) {
+          if (b % GB == 0) {
+            const uint2 v = lds<uint2>(smem, so + (b / GB) * 8);
+            f[i] = __uint_as_float(v.x);
+            c[i] = v.y;
+          }
+        } else if constexpr (FMT == MOE_W_MXFP4) {
+          f[i] = lds<float>(smem, so + b * 4);
+          c[i] = kBf16Back;
+        } else {
+          c[i] = lds<uint32_t>(smem, so + b * 8);
+        }
+        const uint32_t w = lds<uint32_t>(smem, ca + i * 8 * geo.cpitch + b * 16);
+        a[i / 2][i % 2][0] = pair_of<FMT, BF16, 0>(w, c[i]);
+        a[i / 2][i % 2][1] = pair_of<FMT, BF16, 1>(w, c[i]);
+        a[i / 2][i % 2][2] = pair_of<FMT, BF16, 2>(w, c[i]);
+        a[i / 2][i % 2][3] = pair_of<FMT, BF16, 3>(w, c[i]);
+      }
+      constexpr bool POST = FMT != MOE_W_NVFP4;                      // the scale multiplies the group's sum
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const uint4 v = lds<uint4>(smem, xa[nt] + b * 64);
+        uint32_t x0 = v.x, x1 = v.y, x2 = v.z, x3 = v.w;
+        if constexpr (FMT == MOE_W_INT4) {
+          x0 = __byte_perm(v.x, v.z, 0x5410);
+          x1 = __byte_perm(v.x, v.z, 0x7632);
+          x2 = __byte_perm(v.y, v.w, 0x5410);
+          x3 = __byte_perm(v.y, v.w, 0x7632);
+        }
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+          float (&d)[4] = POST ? part[rt][nt] : acc[rt][nt];
+          if (POST && b % GB == 0)
+            mma16816<BF16, true>(d, a[rt][0][0], a[rt][1][0], a[rt][0][1], a[rt][1][1], x0, x1);
+          else
+            mma16816<BF16, false>(d, a[rt][0][0], a[rt][1][0], a[rt][0][1], a[rt][1][1], x0, x1);
+          mma16816<BF16, false>(d, a[rt][0][2], a[rt][1][2], a[rt][0][3], a[rt][1][3], x2, x3);
+          if (POST && (b + 1) % GB == 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[rt][nt][i] = fmaf(d[i], f[2 * rt + i / 2], acc[rt][nt][i]);
+          }
+        }
+      }
+    }
+  }
+  if constexpr (FMT == MOE_W_NVFP4) {
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[rt][nt][i] *= P.tensor_scale;
+  }
+
+  // the warps' sums over K, added in the order of the slices
+  if (geo.wk > 1) {
+    cp_wait(0);
+    __syncthreads();
+    float* red = reinterpret_cast<float*>(smem) + lane;
+    const int wt = 8 / geo.wk, mine = warp & (wt - 1);               // warps of one slice
+    if (wk > 0) {
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            red[((((wk - 1) * wt + mine) * RT + rt) * NT + nt) * 128 + i * 32] = acc[rt][nt][i];
+    }
+    __syncthreads();
+    if (wk > 0) return;
+    for (int w = 0; w < geo.wk - 1; ++w)
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[rt][nt][i] += red[(((w * wt + mine) * RT + rt) * NT + nt) * 128 + i * 32];
+  }
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    const int tile = tile0 + wm * RT + rt;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int t = tok0 + (wn * NT + nt) * 8 + t4 * 2;
+      const float (&v)[4] = acc[rt][nt];
+      if (P.swiglu) {
+        const int n = tile * 8 + g;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (n < P.N / 2 && t + i < P.T) store_y<BF16>(P, t + i, n, v[i] / (1.f + expf(-v[i])) * v[2 + i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int n = tile * 16 + g + (i >> 1) * 8;
+          if (n < P.N && t + (i & 1) < P.T) store_y<BF16>(P, t + (i & 1), n, v[i]);
+        }
+      }
+    }
+  }
+}
+
+constexpr int kSmemMax = 227 * 1024;
+
+template <int FMT, int GROUP, bool BF16, int NT, int RT>
+cudaError_t launch(LinearParams P, const DeviceInfo& dev, cudaStream_t s) {
+  using G = Geometry<FMT, GROUP, BF16, NT, RT>;
+  auto kern = linear_w4_kernel<FMT, GROUP, BF16, NT, RT>;
+  static bool done[64] = {};
+  if (!done[dev.id]) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+    if (e != cudaSuccess) return e;
+    done[dev.id] = true;
+  }
+  const int per16 = P.swiglu ? 8 : 16, outs = P.swiglu ? P.N / 2 : P.N;
+  const int tiles = (outs + per16 - 1) / per16;
+  // Rows per CTA: the most that still give the SMs a CTA and a half each.  Fewer
+  // rows mean more warps along K and a longer stage of x, so not so few that a
+  // stage is longer than K or its x more than twice its codes.
+  if (RT == 1) {
+    P.wn_bits = 0;
+    P.wm_bits = 3;
+    while (P.wm_bits > 0 && (tiles >> P.wm_bits) * 2 < dev.sm_count * 3 && (G::KW << (3 - P.wm_bits)) < P.K &&
+           P.T <= 4 << P.wm_bits)
+      --P.wm_bits;
+  } else {
+    P.wm_bits = 2;
+    P.wn_bits = P.T > 8 * NT ? 1 : 0;
+  }
+  P.x_rows = P.T < (8 * NT << P.wn_bits) ? P.T : 8 * NT << P.wn_bits;
+  P.stages = 2;
+  P.ring = 1;
+  G geo(P);
+  const int nst = (P.K + geo.ks - 1) / geo.ks;
+  P.ring = nst < 2 ? nst : 2;
+  const dim3 grid((tiles + geo.m / 16 - 1) / (geo.m / 16), (P.T + geo.tokens - 1) / geo.tokens);
+  // As deep a ring as lets two CTAs share an SM, or one where one is all there is.
+  const bool two = RT == 1 && static_cast<int64_t>(grid.x) * grid.y > dev.sm_count;
+  for (int n = 3; n <= kMaxStages && n <= nst + 1; ++n) {
+    LinearParams q = P;
+    q.stages = n;
+    q.ring = nst < n ? nst : n;
+    if (G(q).bytes > (two ? kSmemMax / 2 - 1024 : kSmemMax)) break;
+    P = q;
+  }
+  geo = G(P);
+  const int red = (geo.wk - 1) * (8 / geo.wk) * RT * NT * 512;       // the warps' sums use the same memory
+  const int bytes = geo.bytes > red ? geo.bytes : red;
+  const cudaError_t e = launch_pdl(kern, grid, dim3(kThreads), bytes, s, P);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// Tokens per warp: NT tiles of 8.  Above 32 tokens a warp takes 32 rows (RT = 2)
+// so that the x operand is read from shared memory once for two row tiles.
+template <int FMT, int GROUP, bool BF16>
+cudaError_t launch_tokens(const LinearParams& P, const DeviceInfo& dev, cudaStream_t s) {
+  if (P.T <= 8) return launch<FMT, GROUP, BF16, 1, 1>(P, dev, s);
+  if (P.T <= 16) return launch<FMT, GROUP, BF16, 2, 1>(P, dev, s);
+  if (P.T <= 32) return launch<FMT, GROUP, BF16, 4, 1>(P, dev, s);
+  return launch<FMT, GROUP, BF16, 8, 2>(P, dev, s);
+}
+
+}  // namespace w4
+}  // namespace moe
