@@ -18,9 +18,13 @@
 //
 // K order.  The MMA's k slots may hold any 16 elements as long as both operands
 // agree.  A quad's four threads hold 8 consecutive k each, 32 in all: two MMAs.
-// INT4: masking the halves of a shifted word yields the pairs (k, k+4), ...,
-// (k+3, k+7); the words of x are permuted alike.  E2M1: a byte converts to the
-// pair (k, k+1), x as it is.
+// Masking the halves of a shifted word yields the pairs (k, k+4), ..., (k+3, k+7)
+// and the words of x are permuted alike; where E2M1 converts to f16 by the byte,
+// the pairs are (k, k+1), ... and x stays as it is.
+//
+// Rows in shared memory: the CTA's M rows in order, or with SwiGLU M/2 gate rows
+// and then the M/2 up rows of the same outputs.  A 16-row MMA tile takes 8 of
+// each, so that a thread's accumulators hold h and u of one output.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -41,7 +45,7 @@ struct LinearParams {
   int N, K, T, groups, scale_type, y_f32, swiglu, accumulate;
   float tensor_scale;
   // launch shape
-  int wm_bits, wn_bits;    // warps along the rows and the tokens (log2); the other warps split K
+  int wm_bits;             // warps along the rows (log2); the warps left over split K
   int stages, ring;        // stages in flight + 1; slots (no more than there are stages)
   int x_rows;              // token rows a stage holds
 };
@@ -112,25 +116,36 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
   return r;
 }
 
+// (a & b) | c, with the constants in registers: one instruction.
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+
 // Pair I (0..3) of a word as two exact values of the x type.
 //   INT4: `c` holds (M + zero, M + zero) with M = 128 (bf16) or 1024 (f16), where
 //   the type's step is 1, and a code is OR-ed into M's low bits.
-//   E2M1: the conversion to f16; for bf16 the exponent and the top of the
-//   mantissa move 3 places down, which reads as the value * 2^-112; `c` takes
-//   that back, and multiplies with NVFP4's block scale.
+//   E2M1, f16: converted by the byte.
+//   E2M1, bf16: sign and (exponent, mantissa) move to their places; the format's
+//   subnormals are the type's, so the bits read as the value * 2^-126, which `c`
+//   takes back (in part, where it multiplies with NVFP4's block scale: kNvBack).
 template <int FMT, bool BF16, int I>
 __device__ __forceinline__ uint32_t pair_of(uint32_t w, uint32_t c) {
   if constexpr (FMT == MOE_W_INT4) {
-    constexpr uint32_t M = BF16 ? 0x43004300u : 0x64006400u;
-    return sub2<BF16>(((w >> (4 * I)) & 0x000F000Fu) | M, c);
+    return sub2<BF16>(and_or(w >> (4 * I), 0x000F000Fu, BF16 ? 0x43004300u : 0x64006400u), c);
+  } else if constexpr (BF16) {
+    const uint32_t sign = w << (12 - 4 * I);
+    const uint32_t mag = (I < 2 ? w << (I < 2 ? 6 - 4 * I : 0) : w >> (I < 2 ? 0 : 4 * I - 6)) & 0x01C001C0u;
+    return mul2<true>(and_or(sign, 0x80008000u, mag), c);
   } else {
     uint32_t h;
     asm("{ .reg .b8 b; cvt.u8.u32 b, %1; cvt.rn.f16x2.e2m1x2 %0, b; }" : "=r"(h) : "r"(w >> (8 * I)));
-    if constexpr (BF16) return mul2<true>((h & 0x80008000u) | ((h >> 3) & 0x0FFF0FFFu), c);
     return FMT == MOE_W_NVFP4 ? mul2<false>(h, c) : h;
   }
 }
-constexpr uint32_t kBf16Back = 0x77807780u;   // 2^112 twice
+constexpr uint32_t kMxBack = 0x7E807E80u;     // 2^126 twice
+constexpr float kNvPart = 1.298074214633707e33f, kNvBack = 65536.f;   // 2^110, 2^16 (a scale times 2^126 overflows)
 
 // E8M0: 2^(b - 127); 0 is a subnormal of fp32, 255 is NaN.
 __device__ __forceinline__ float e8m0_value(uint32_t b) {
@@ -142,19 +157,9 @@ template <bool BF16>
 __device__ __forceinline__ uint32_t e4m3_mult(uint32_t b) {
   const __half h = __half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(b), __NV_E4M3));
   uint32_t u;
-  if constexpr (BF16) u = __float_as_uint(__half2float(h) * 5.192296858534828e33f) >> 16;   // * 2^112
+  if constexpr (BF16) u = __float_as_uint(__half2float(h) * kNvPart) >> 16;
   else u = __half_as_ushort(h);
   return u | (u << 16);
-}
-
-// Row of W that tile row r of the 16-row tile `tile` holds (clamped to the last
-// one): with SwiGLU rows 0-7 are gate rows and 8-15 the up rows of the same outputs.
-__device__ __forceinline__ int weight_row(const LinearParams& P, int tile, int r) {
-  if (P.swiglu) {
-    const int half = P.N >> 1, i = min(tile * 8 + (r & 7), half - 1);
-    return r < 8 ? i : half + i;
-  }
-  return min(tile * 16 + r, P.N - 1);
 }
 
 template <bool BF16>
@@ -172,23 +177,26 @@ __device__ __forceinline__ void store_y(const LinearParams& P, int t, int n, flo
   }
 }
 
-// GROUP: elements of K per scale.  KW: elements of K a warp takes from a stage.
-template <int FMT, int GROUP, bool BF16, int NT, int RT>
+// GROUP: elements of K per scale; NT, RT: 8-token and 16-row tiles of a warp; WN:
+// warps along the tokens.
+template <int FMT, int GROUP, bool BF16, int NT, int RT, int WN>
 struct Geometry {
-  static constexpr int KW = RT == 1 ? 256 : 128;
-  static constexpr int STAGE_WEIGHTS = 8 * 16 * RT * KW;                // at one warp tile of tokens
-  static constexpr int EPT = STAGE_WEIGHTS / GROUP / kThreads;          // scales a thread fetches per stage
+  static constexpr int KW = NT == 8 ? 128 : 256;                        // K a warp takes from a stage
+  static constexpr int STAGE_WEIGHTS = 8 / WN * 16 * RT * KW;
+  static constexpr int SCALES = STAGE_WEIGHTS / GROUP;
+  static constexpr int EPT = SCALES < kThreads ? 1 : SCALES / kThreads; // scales a thread fetches per stage
   static constexpr int CPT = STAGE_WEIGHTS / 32 / kThreads;             // 16-byte chunks of codes a thread copies
   static constexpr int ENTRY = FMT == MOE_W_INT4 ? 8 : 4;               // bytes of a scale in shared memory
-  int wk, ks, m, tokens, gps, cpitch, xpitch, spitch, stage, sbuf, zero_at, s_at, bytes;
+  static_assert(CPT >= 2, "a thread copies rows of both parts");
+  int wk, ks, m, gps, cpitch, xpitch, spitch, stage, sbuf, zero_at, s_at, bytes;
   // wk: warps along K; ks: K per stage; m: rows; gps: groups of a row per stage;
   // pitches: bytes of a row of codes (conflict-free 4-byte reads of 8 rows), of x
   // (16-byte reads of 2 rows) and of scales (odd in entries)
+  static constexpr int TOKENS = 8 * NT * WN;
   __host__ __device__ explicit Geometry(const LinearParams& P) {
-    wk = 8 >> P.wm_bits >> P.wn_bits;
+    wk = (8 / WN) >> P.wm_bits;
     ks = KW * wk;
     m = 16 * RT << P.wm_bits;
-    tokens = 8 * NT << P.wn_bits;
     gps = ks / GROUP;
     cpitch = ks / 2 + 16;
     xpitch = ks * 2 + 64;
@@ -201,57 +209,65 @@ struct Geometry {
   }
 };
 
-template <int FMT, int GROUP, bool BF16, int NT, int RT>
-__global__ void __launch_bounds__(kThreads, RT == 1 ? 2 : 1) linear_w4_kernel(const __grid_constant__ LinearParams P) {
-  using G = Geometry<FMT, GROUP, BF16, NT, RT>;
+template <int FMT, int GROUP, bool BF16, int NT, int RT, int WN>
+__global__ void __launch_bounds__(kThreads, NT < 8 ? 2 : 1) linear_w4_kernel(const __grid_constant__ LinearParams P) {
+  using G = Geometry<FMT, GROUP, BF16, NT, RT, WN>;
   constexpr int KW = G::KW, KB = KW / 32, GB = GROUP >= 32 ? GROUP / 32 : 1;
+  constexpr bool PERMUTE = FMT == MOE_W_INT4 || BF16;                // x pairs (k, k+4): see pair_of
   extern __shared__ __align__(16) unsigned char smem[];
   const G geo(P);
   const uint32_t sm = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
-  const int wm = warp & ((1 << P.wm_bits) - 1), wn = (warp >> P.wm_bits) & ((1 << P.wn_bits) - 1);
-  const int wk = warp >> P.wm_bits >> P.wn_bits;
-  const int tile0 = blockIdx.x * (geo.m / 16);                       // first 16-row tile of the CTA
-  const int tok0 = blockIdx.y * geo.tokens;
+  const int wm = warp & ((1 << P.wm_bits) - 1), wn = WN == 1 ? 0 : (warp >> P.wm_bits) & (WN - 1);
+  const int wk = warp >> P.wm_bits >> (WN - 1);                      // WN is 1 or 2
+  const int tok0 = blockIdx.y * G::TOKENS;
   const int x_rows = min(P.x_rows, P.T - tok0);
   const int nst = (P.K + geo.ks - 1) / geo.ks;
+  // Row r of shared memory is row first + r of W for r below `split`, else row
+  // up + r - split (SwiGLU); rows from `valid` of each part on are not there.
+  const int split = P.swiglu ? geo.m / 2 : geo.m, outs = P.swiglu ? P.N >> 1 : P.N;
+  const int first = blockIdx.x * split, valid = min(split, outs - first);
   pdl_wait();
   pdl_trigger();
+
+  // A thread's rows of a kind (codes, scales) are r0, r0 + step, ... ; n of them
+  // in all.  The first half of them lies in the first part, the second half in
+  // the second one (a single row lies where it does).
+  auto row_of = [&](int r) { return r < split || !P.swiglu ? first + r : outs + first + r - split; };
+  auto there = [&](int r) { return (r < split || !P.swiglu ? r : r - split) < valid; };
 
   // A stage's copies: thread -> 16-byte chunk `col` of every code_rows-th row (a
   // row of codes has a power of two <= 64 chunks, a row of x four times as many).
   const int cpr_bits = 31 - __clz(geo.ks / 32), col = tid & ((1 << cpr_bits) - 1);
   const int code_rows = kThreads >> cpr_bits, code_r = tid >> cpr_bits;
-  const uint8_t* src[G::CPT];
+  const uint8_t* csrc[2];
+  unsigned cok = 0;                                                  // which rows are there
 #pragma unroll
-  for (int i = 0; i < G::CPT; ++i) {
-    const int r = min(i * code_rows + code_r, geo.m - 1);
-    src[i] = P.codes + static_cast<size_t>(weight_row(P, tile0 + (r >> 4), r & 15)) * (P.K >> 1) + col * 16;
-  }
+  for (int i = 0; i < G::CPT; ++i) cok |= there(i * code_rows + code_r) << i;
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    csrc[h] = P.codes + static_cast<size_t>(row_of(h * (G::CPT / 2) * code_rows + code_r)) * (P.K >> 1) + col * 16;
+  const size_t cstep = static_cast<size_t>(code_rows) * (P.K >> 1);
   const int xpr_bits = cpr_bits + 2, xcol = tid & ((1 << xpr_bits) - 1);
   const int xrow_step = kThreads >> xpr_bits, xr0 = tid >> xpr_bits;
   const uint16_t* xsrc = static_cast<const uint16_t*>(P.x) + static_cast<int64_t>(tok0 + xr0) * P.ldx + xcol * 8;
   const int64_t xstep = xrow_step * P.ldx;
-  const uint32_t cdst = sm + code_r * geo.cpitch + col * 16;
-  const uint32_t xdst = sm + geo.m * geo.cpitch + xr0 * geo.xpitch + xcol * 16;
+  const uint32_t cdst = sm + code_r * geo.cpitch + col * 16, cdstep = code_rows * geo.cpitch;
+  const uint32_t xdst = sm + geo.m * geo.cpitch + xr0 * geo.xpitch + xcol * 16, xdstep = xrow_step * geo.xpitch;
   int slot_in = 0;                                                   // slot of the next stage to issue
   auto issue = [&](int st) {
     if (st < nst) {
       const int k0 = st * geo.ks;
       const uint32_t at = slot_in * geo.stage;
-      const bool ok = k0 + col * 32 < P.K;
+      // behind K zeros are written and nothing is read (from the row's start)
+      const bool ok = k0 + col * 32 < P.K, xok = k0 + xcol * 8 < P.K;
+      const int64_t off = ok ? k0 >> 1 : -col * 16;
 #pragma unroll
       for (int i = 0; i < G::CPT; ++i)
-        if (i * code_rows + code_r < geo.m)
-          cp_async16(cdst + at + i * code_rows * geo.cpitch, ok ? src[i] + (k0 >> 1) : P.codes, ok);
-      const bool xok = k0 + xcol * 8 < P.K;
-      const uint16_t* xp = xsrc + k0;
+        if (cok >> i & 1) cp_async16(cdst + at + i * cdstep, csrc[2 * i / G::CPT] + off + i % (G::CPT / 2) * cstep, ok);
+      const uint16_t* xp = xsrc + (xok ? k0 : -xcol * 8);
       uint32_t xd = xdst + at;
-      for (int r = xr0; r < x_rows; r += xrow_step) {
-        cp_async16(xd, xok ? static_cast<const void*>(xp) : P.x, xok);
-        xp += xstep;
-        xd += xrow_step * geo.xpitch;
-      }
+      for (int r = xr0; r < x_rows; r += xrow_step, xp += xstep, xd += xdstep) cp_async16(xd, xp, xok);
       slot_in = slot_in + 1 == P.ring ? 0 : slot_in + 1;
     }
     cp_commit();
@@ -261,21 +277,25 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 2 : 1) linear_w4_kernel(co
   // Scales of a stage: thread -> group `sg` of every s_rows-th row; raw values in registers.
   const int gps_bits = 31 - __clz(geo.gps), sg = tid & (geo.gps - 1);
   const int s_rows = kThreads >> gps_bits, s_r = tid >> gps_bits;
-  int srow[G::EPT];
+  constexpr int EH = G::EPT > 1 ? G::EPT / 2 : 1;
+  size_t ssrc[2];
+  unsigned sok = 0;
 #pragma unroll
-  for (int i = 0; i < G::EPT; ++i) {
-    const int r = min(i * s_rows + s_r, geo.m - 1);
-    srow[i] = weight_row(P, tile0 + (r >> 4), r & 15);
-  }
+  for (int i = 0; i < G::EPT; ++i) sok |= (s_r < geo.m && there(i * s_rows + s_r)) << i;
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    ssrc[h] = static_cast<size_t>(row_of(min(h * EH * s_rows + s_r, geo.m - 1))) * P.groups + sg;
+  const size_t sstep = static_cast<size_t>(s_rows) * P.groups;
   uint32_t sraw[G::EPT], zraw[G::EPT];
   auto fetch = [&](int st) {
-    const int j = st * geo.gps + sg;
+    const int j = st * geo.gps;
+    const bool in = j + sg < P.groups;
 #pragma unroll
     for (int i = 0; i < G::EPT; ++i) {
       sraw[i] = 0;
       zraw[i] = 8;
-      if (j < P.groups) {
-        const size_t at = static_cast<size_t>(static_cast<uint32_t>(srow[i])) * static_cast<uint32_t>(P.groups) + j;
+      if (in && (sok >> i & 1)) {
+        const size_t at = ssrc[i / EH] + j + i % EH * sstep;
         if constexpr (FMT == MOE_W_INT4) {
           sraw[i] = P.scale_type == MOE_DT_F32 ? __ldg(static_cast<const uint32_t*>(P.scales) + at)
                                                : __ldg(static_cast<const uint16_t*>(P.scales) + at);
@@ -289,9 +309,9 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 2 : 1) linear_w4_kernel(co
   unsigned char* const sdst = smem + geo.s_at + s_r * geo.spitch + sg * G::ENTRY;
   auto put = [&](int st) {
     unsigned char* d = sdst + (st & 1) * geo.sbuf;
+    if (G::SCALES < kThreads && s_r >= geo.m) return;
 #pragma unroll
     for (int i = 0; i < G::EPT; ++i, d += s_rows * geo.spitch) {
-      if (i * s_rows + s_r >= geo.m) break;
       if constexpr (FMT == MOE_W_INT4) {
         const uint32_t f = P.scale_type == MOE_DT_F32    ? sraw[i]
                            : P.scale_type == MOE_DT_BF16 ? sraw[i] << 16
@@ -318,7 +338,8 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 2 : 1) linear_w4_kernel(co
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[rt][nt][i] = 0.f;
 
-  const int row = wm * 16 * RT + g;                                  // this thread's rows: row + 8 i
+  // this thread's rows in shared memory: row + rt * rt_step + i * i_step, i = 0, 1
+  const int rt_step = P.swiglu ? 8 : 16, i_step = P.swiglu ? split : 8, row = wm * RT * rt_step + g;
   const uint32_t code_at = row * geo.cpitch + wk * (KW / 2) + t4 * 4;
   const uint32_t scale_at = geo.s_at + row * geo.spitch +
                             (wk * (KW / GROUP) + (FMT == MOE_W_NVFP4 ? t4 >> 1 : 0)) * G::ENTRY;
@@ -345,7 +366,8 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 2 : 1) linear_w4_kernel(co
       uint32_t a[RT][2][4];
 #pragma unroll
       for (int i = 0; i < 2 * RT; ++i) {
-        const uint32_t so = sa + i * 8 * geo.spitch;
+        const int dr = (i / 2) * rt_step + (i % 2) * i_step;
+        const uint32_t so = sa + dr * geo.spitch;
         if constexpr (FMT == MOE_W_INT4) {
           if (b % GB == 0) {
             const uint2 v = lds<uint2>(smem, so + (b / GB) * 8);
@@ -354,11 +376,11 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 2 : 1) linear_w4_kernel(co
           }
         } else if constexpr (FMT == MOE_W_MXFP4) {
           f[i] = lds<float>(smem, so + b * 4);
-          c[i] = kBf16Back;
+          c[i] = kMxBack;
         } else {
           c[i] = lds<uint32_t>(smem, so + b * 8);
         }
-        const uint32_t w = lds<uint32_t>(smem, ca + i * 8 * geo.cpitch + b * 16);
+        const uint32_t w = lds<uint32_t>(smem, ca + dr * geo.cpitch + b * 16);
         a[i / 2][i % 2][0] = pair_of<FMT, BF16, 0>(w, c[i]);
         a[i / 2][i % 2][1] = pair_of<FMT, BF16, 1>(w, c[i]);
         a[i / 2][i % 2][2] = pair_of<FMT, BF16, 2>(w, c[i]);
@@ -369,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 2 : 1) linear_w4_kernel(co
       for (int nt = 0; nt < NT; ++nt) {
         const uint4 v = lds<uint4>(smem, xa[nt] + b * 64);
         uint32_t x0 = v.x, x1 = v.y, x2 = v.z, x3 = v.w;
-        if constexpr (FMT == MOE_W_INT4) {
+        if constexpr (PERMUTE) {
           x0 = __byte_perm(v.x, v.z, 0x5410);
           x1 = __byte_perm(v.x, v.z, 0x7632);
           x2 = __byte_perm(v.y, v.w, 0x5410);
@@ -397,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 2 : 1) linear_w4_kernel(co
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[rt][nt][i] *= P.tensor_scale;
+        for (int i = 0; i < 4; ++i) acc[rt][nt][i] *= BF16 ? kNvBack * P.tensor_scale : P.tensor_scale;
   }
 
   // the warps' sums over K, added in the order of the slices
@@ -427,22 +449,18 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 2 : 1) linear_w4_kernel(co
   }
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
-    const int tile = tile0 + wm * RT + rt;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int t = tok0 + (wn * NT + nt) * 8 + t4 * 2;
+      const int t = tok0 + (wn * NT + nt) * 8 + t4 * 2, r = row + rt * rt_step;
       const float (&v)[4] = acc[rt][nt];
       if (P.swiglu) {
-        const int n = tile * 8 + g;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          if (n < P.N / 2 && t + i < P.T) store_y<BF16>(P, t + i, n, v[i] / (1.f + expf(-v[i])) * v[2 + i]);
+          if (r < valid && t + i < P.T) store_y<BF16>(P, t + i, first + r, v[i] / (1.f + expf(-v[i])) * v[2 + i]);
       } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int n = tile * 16 + g + (i >> 1) * 8;
-          if (n < P.N && t + (i & 1) < P.T) store_y<BF16>(P, t + (i & 1), n, v[i]);
-        }
+        for (int i = 0; i < 4; ++i)
+          if (r + (i >> 1) * 8 < valid && t + (i & 1) < P.T) store_y<BF16>(P, t + (i & 1), first + r + (i >> 1) * 8, v[i]);
       }
     }
   }
@@ -450,40 +468,39 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 2 : 1) linear_w4_kernel(co
 
 constexpr int kSmemMax = 227 * 1024;
 
-template <int FMT, int GROUP, bool BF16, int NT, int RT>
+template <int FMT, int GROUP, bool BF16, int NT, int RT, int WN>
 cudaError_t launch(LinearParams P, const DeviceInfo& dev, cudaStream_t s) {
-  using G = Geometry<FMT, GROUP, BF16, NT, RT>;
-  auto kern = linear_w4_kernel<FMT, GROUP, BF16, NT, RT>;
+  using G = Geometry<FMT, GROUP, BF16, NT, RT, WN>;
+  auto kern = linear_w4_kernel<FMT, GROUP, BF16, NT, RT, WN>;
   static bool done[64] = {};
   if (!done[dev.id]) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
     if (e != cudaSuccess) return e;
     done[dev.id] = true;
   }
-  const int per16 = P.swiglu ? 8 : 16, outs = P.swiglu ? P.N / 2 : P.N;
-  const int tiles = (outs + per16 - 1) / per16;
+  const int tiles = (P.N + 15) / 16;
   // Rows per CTA: the most that still give the SMs a CTA and a half each.  Fewer
   // rows mean more warps along K and a longer stage of x, so not so few that a
   // stage is longer than K or its x more than twice its codes.
-  if (RT == 1) {
-    P.wn_bits = 0;
-    P.wm_bits = 3;
-    while (P.wm_bits > 0 && (tiles >> P.wm_bits) * 2 < dev.sm_count * 3 && (G::KW << (3 - P.wm_bits)) < P.K &&
-           P.T <= 4 << P.wm_bits)
-      --P.wm_bits;
-  } else {
-    P.wm_bits = 2;
-    P.wn_bits = P.T > 8 * NT ? 1 : 0;
+  P.x_rows = P.T < G::TOKENS ? P.T : G::TOKENS;
+  P.wm_bits = NT < 8 ? 3 : 2;
+  while (NT < 8 && P.wm_bits > 0 && (tiles / RT >> P.wm_bits) * 2 < dev.sm_count * 3) {
+    LinearParams q = P;
+    --q.wm_bits;
+    q.ring = 2;
+    const G geo(q);
+    if (geo.ks / 2 >= P.K || P.x_rows * geo.ks * 4 > geo.m * geo.ks * 2 || geo.bytes > kSmemMax) break;
+    P.wm_bits = q.wm_bits;
   }
-  P.x_rows = P.T < (8 * NT << P.wn_bits) ? P.T : 8 * NT << P.wn_bits;
   P.stages = 2;
   P.ring = 1;
   G geo(P);
   const int nst = (P.K + geo.ks - 1) / geo.ks;
   P.ring = nst < 2 ? nst : 2;
-  const dim3 grid((tiles + geo.m / 16 - 1) / (geo.m / 16), (P.T + geo.tokens - 1) / geo.tokens);
+  const int per = P.swiglu ? geo.m / 2 : geo.m, outs = P.swiglu ? P.N / 2 : P.N;
+  const dim3 grid((outs + per - 1) / per, (P.T + G::TOKENS - 1) / G::TOKENS);
   // As deep a ring as lets two CTAs share an SM, or one where one is all there is.
-  const bool two = RT == 1 && static_cast<int64_t>(grid.x) * grid.y > dev.sm_count;
+  const bool two = NT < 8 && static_cast<int64_t>(grid.x) * grid.y > dev.sm_count;
   for (int n = 3; n <= kMaxStages && n <= nst + 1; ++n) {
     LinearParams q = P;
     q.stages = n;
@@ -498,14 +515,19 @@ cudaError_t launch(LinearParams P, const DeviceInfo& dev, cudaStream_t s) {
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// Tokens per warp: NT tiles of 8.  Above 32 tokens a warp takes 32 rows (RT = 2)
-// so that the x operand is read from shared memory once for two row tiles.
+// Tokens per warp: NT tiles of 8.  A warp takes 32 rows (RT = 2), so that x is
+// read from shared memory and permuted once for two row tiles, unless that leaves
+// SMs without a CTA.
 template <int FMT, int GROUP, bool BF16>
 cudaError_t launch_tokens(const LinearParams& P, const DeviceInfo& dev, cudaStream_t s) {
-  if (P.T <= 8) return launch<FMT, GROUP, BF16, 1, 1>(P, dev, s);
-  if (P.T <= 16) return launch<FMT, GROUP, BF16, 2, 1>(P, dev, s);
-  if (P.T <= 32) return launch<FMT, GROUP, BF16, 4, 1>(P, dev, s);
-  return launch<FMT, GROUP, BF16, 8, 2>(P, dev, s);
+  const bool wide = P.N >= 64 * dev.sm_count;
+  if (P.T <= 8)
+    return wide ? launch<FMT, GROUP, BF16, 1, 2, 1>(P, dev, s) : launch<FMT, GROUP, BF16, 1, 1, 1>(P, dev, s);
+  if (P.T <= 16)
+    return wide ? launch<FMT, GROUP, BF16, 2, 2, 1>(P, dev, s) : launch<FMT, GROUP, BF16, 2, 1, 1>(P, dev, s);
+  if (P.T <= 32) return launch<FMT, GROUP, BF16, 4, 1, 1>(P, dev, s);
+  if (P.T <= 64) return launch<FMT, GROUP, BF16, 8, 2, 1>(P, dev, s);
+  return launch<FMT, GROUP, BF16, 8, 2, 2>(P, dev, s);
 }
 
 }  // namespace w4
