@@ -25,7 +25,6 @@ MOE_FFN_ACT_NVFP4 = 1
 MOE_W_INT4 = 3
 LINEAR_FORMATS = {"mxfp4": MOE_W_MXFP4, "nvfp4": MOE_W_NVFP4, "int4": MOE_W_INT4}
 MOE_DT_F32, MOE_DT_BF16, MOE_DT_F16 = 0, 1, 2
-DTYPES = {torch.float32: MOE_DT_F32, torch.bfloat16: MOE_DT_BF16, torch.float16: MOE_DT_F16}
 MOE_LINEAR_SWIGLU, MOE_LINEAR_ACCUMULATE = 1, 2
 
 
@@ -290,56 +289,28 @@ def moe_layer_forward(s: moe_shape, logits, x, k: int, idx, gate, offsets, perm,
                                    _ptr(out), _ptr(dev_status), _stream(stream)))
 
 
-# The calls below are short kernels, so the host's share of a call counts: every
-# tensor is checked and resolved to its address in one pass (_mem), on the
-# current device, and the stream is taken without building a torch.cuda.Stream.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# The calls below are short kernels, so the host's share of a call counts: their
+# tensors are checked and handed to the library in C++ (native.cpp).
+_nat = None
 
 
-def _mem(name, t, n, dtype, dev):
-    """Address of a contiguous tensor on CUDA device `dev` of the documented
-    dtype with the n elements the call touches; None for None."""
-    if t is None:
-        return None
-    if t.get_device() != dev or t.dtype is not dtype or t.numel() < n or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of >= {n} elements on the current device "
-                         f"cuda:{dev}, got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
-    return t.data_ptr()
+def _load_native():
+    """The extension of the short calls; raises if it has not been built."""
+    global _nat
+    if _nat is None:
+        lib()
+        try:
+            from . import _native as n
+        except ImportError as e:
+            raise ImportError(f"{os.path.join(_HERE, '_native.so')} cannot be loaded ({e}): build it with "
+                              "`python -m expert_offload_serving_b200.build`") from e
+        _nat = n
+    return _nat
 
 
-def _matrix(name, t, rows, cols, dtype, dev):
-    """_mem of a tensor of exactly [rows, cols]."""
-    if t is None:
-        return None
-    if t.shape != (rows, cols) or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {(rows, cols)} on the current device "
-                         f"cuda:{dev}, got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
-    return t.data_ptr()
-
-
-def _rows(name, t, shape, dev):
-    """Row distance of a matrix of `shape` on the device whose rows are
-    contiguous and do not overlap."""
-    st = t.stride()
-    n, width = shape
-    if t.get_device() != dev or t.shape != shape or (st[1] != 1 and width > 1) or (st[0] < width and n > 1):
-        raise ValueError(f"{name}: expected a {tuple(shape)} tensor with contiguous rows on the current device "
-                         f"cuda:{dev}, got {t.dtype} {tuple(t.shape)} with strides {st} on {t.device}")
-    return st[0] if n > 1 else (width + 7) // 8 * 8       # a single row has no distance
-
-
-def _device_of(name, t):
-    """The current device, which has to be the one that t is on."""
-    dev = t.get_device()
-    if dev < 0 or dev != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}: expected the current CUDA device")
-    return dev
-
-
-def _current(stream, dev):
-    if stream is None and _raw_stream is not None:
-        return _raw_stream(dev)
-    return _stream(stream)
+def _done(status: int):
+    if status != MOE_OK:
+        raise MoeError(status, _nat.last_error())
 
 
 def moe_linear_w4(x, codes, scales, out, fmt="int4", group: int = 128, zeros=None, tensor_scale: float = 1.0,
@@ -350,40 +321,10 @@ def moe_linear_w4(x, codes, scales, out, fmt="int4", group: int = 128, zeros=Non
     "nvfp4" (scales uint8, group 32 or 16).  x [T, K] bf16 or fp16, out [T, N] of
     x's type or fp32; rows of both may be any distance apart.  swiglu: out
     [T, N/2] = silu(h) * u of W's two row halves."""
-    f = LINEAR_FORMATS[fmt]
-    dev = _device_of("x", x)
-    T, K = x.shape
-    N = codes.shape[0]
-    if group <= 0:
-        raise ValueError(f"group={group}")
-    G = -(-K // group)
-    sdt = scales.dtype
-    if f == MOE_W_INT4 and sdt not in DTYPES:
-        raise ValueError(f"scales: expected float32, bfloat16 or float16, got {sdt}")
-    if x.dtype not in DTYPES or out.dtype not in DTYPES:
-        raise ValueError(f"x {x.dtype}, out {out.dtype}: expected bfloat16 or float16, and that or float32")
-    pc = _matrix("codes", codes, N, K // 2, torch.uint8, dev)
-    ps = _matrix("scales", scales, N, G, sdt if f == MOE_W_INT4 else torch.uint8, dev)
-    pz = _matrix("zeros", zeros, N, G, torch.uint8, dev)
-    ldx, ldy = _rows("x", x, (T, K), dev), _rows("out", out, (T, N // 2 if swiglu else N), dev)
-    st = (_lib or lib()).moe_linear_w4(
-        moe_linear_shape(N, K, f, group, DTYPES.get(sdt, MOE_DT_F32)), pc, ps, pz, tensor_scale, x.data_ptr(),
-        DTYPES[x.dtype], ldx, T, out.data_ptr(), DTYPES[out.dtype], ldy,
-        (MOE_LINEAR_SWIGLU if swiglu else 0) | (MOE_LINEAR_ACCUMULATE if accumulate else 0), _current(stream, dev))
-    if st:
-        _check(st)
-
-
-def _batch(logits, idx, seq_offsets, mask, dev):
-    """T, E, k, S and the addresses of a routed batch."""
-    T, E = logits.shape
-    k = idx.shape[1]
-    S = 1 if seq_offsets is None else seq_offsets.numel() - 1
-    if mask is not None and mask.dtype is not torch.bool and mask.dtype is not torch.uint8:
-        raise ValueError(f"mask: expected bool or uint8, got {mask.dtype}")
-    return (T, E, k, S, _mem("logits", logits, T * E, torch.float32, dev),
-            _matrix("idx", idx, T, k, torch.int32, dev), _mem("seq_offsets", seq_offsets, S + 1, torch.int32, dev),
-            None if mask is None else _mem("mask", mask, T, mask.dtype, dev))
+    _done((_nat or _load_native()).linear_w4(
+        x, codes, scales, out, zeros, LINEAR_FORMATS[fmt], group, tensor_scale,
+        (MOE_LINEAR_SWIGLU if swiglu else 0) | (MOE_LINEAR_ACCUMULATE if accumulate else 0),
+        None if stream is None else _stream(stream)))
 
 
 def moe_balance_loss_workspace_bytes(T: int, E: int, S: int = 1) -> int:
@@ -395,49 +336,24 @@ def moe_balance_loss(logits, idx, loss, counts, prob, coef, workspace, seq_offse
     """loss [2] = (balance loss, z-loss), counts [S, E] int32, prob [S, E] and
     coef [S + 1] of the routing idx [T, k] of logits [T, E]; seq_offsets int32
     [S + 1] (None: one sequence), mask [T] bool or uint8 (None: every token)."""
-    dev = _device_of("logits", logits)
-    f32 = torch.float32
-    T, E, k, S, pl, pi, po, pm = _batch(logits, idx, seq_offsets, mask, dev)
-    st = (_lib or lib()).moe_balance_loss(
-        pl, T, E, pi, k, po, S, pm, _mem("loss", loss, 2, f32, dev), _mem("counts", counts, S * E, torch.int32, dev),
-        _mem("prob", prob, S * E, f32, dev), _mem("coef", coef, S + 1, f32, dev),
-        _mem("workspace", workspace, 0, torch.uint8, dev), workspace.numel(),
-        _mem("dev_status", dev_status, 1, torch.int32, dev), _current(stream, dev))
-    if st:
-        _check(st)
+    _done((_nat or _load_native()).balance_loss(logits, idx, loss, counts, prob, coef, workspace, seq_offsets, mask, dev_status,
+                                           None if stream is None else _stream(stream)))
 
 
 def moe_router_backward(logits, idx, dlogits, gate=None, dgate=None, counts=None, coef=None, dloss=None,
                         seq_offsets=None, mask=None, dev_status=None, stream=None):
     """dlogits [T, E] of the gates (dgate [T, k]; None: no such term) and of the
     losses (dloss [2], with counts and coef of moe_balance_loss; None: none)."""
-    dev = _device_of("logits", logits)
-    f32 = torch.float32
-    T, E, k, S, pl, pi, po, pm = _batch(logits, idx, seq_offsets, mask, dev)
-    st = (_lib or lib()).moe_router_backward(
-        pl, T, E, pi, _mem("gate", gate, T * k, f32, dev), _mem("dgate", dgate, T * k, f32, dev), k, po, S, pm,
-        _mem("counts", counts, S * E, torch.int32, dev), _mem("coef", coef, S + 1, f32, dev),
-        _mem("dloss", dloss, 2, f32, dev), _mem("dlogits", dlogits, T * E, f32, dev),
-        _mem("dev_status", dev_status, 1, torch.int32, dev), _current(stream, dev))
-    if st:
-        _check(st)
+    _done((_nat or _load_native()).router_backward(logits, idx, dlogits, gate, dgate, counts, coef, dloss, seq_offsets, mask,
+                                              dev_status, None if stream is None else _stream(stream)))
 
 
 def moe_combine_backward(y_perm, idx, gate, inv_perm, slot_of_expert, dout, E: int, dgate, dy_perm=None, stream=None):
     """dgate [T, k] and, if wanted, dy_perm [T*k, d] from dout [T, d], for the
     pairs moe_combine_merge adds (the other pairs' dgate is 0, their dy_perm
     rows stay as they are)."""
-    dev = _device_of("dout", dout)
-    f32, i32 = torch.float32, torch.int32
-    T, k = idx.shape
-    n, d = T * k, dout.shape[1]
-    st = (_lib or lib()).moe_combine_backward(
-        _mem("y_perm", y_perm, n * d, f32, dev), _mem("idx", idx, n, i32, dev), _mem("gate", gate, n, f32, dev),
-        _mem("inv_perm", inv_perm, n, i32, dev), _mem("slot_of_expert", slot_of_expert, E, i32, dev),
-        _mem("dout", dout, T * d, f32, dev), T, k, d, E, _mem("dgate", dgate, n, f32, dev),
-        _mem("dy_perm", dy_perm, n * d, f32, dev), _current(stream, dev))
-    if st:
-        _check(st)
+    _done((_nat or _load_native()).combine_backward(y_perm, idx, gate, inv_perm, slot_of_expert, dout, E, dgate, dy_perm,
+                                               None if stream is None else _stream(stream)))
 
 
 def moe_split_misses(misses, tokens_per_expert, q=None, bw_pcie=0.0, bw_host=0.0):
