@@ -19,6 +19,7 @@
 // (the row is read anyway).  Bound by HBM: 4 E bytes in, 4 E out per token.
 #include <climits>
 #include <cmath>
+#include <type_traits>
 
 #include "common.cuh"
 
@@ -72,9 +73,9 @@ struct BalanceWs {
 };
 
 __device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
-  return v;
+  float r;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
 }
 template <typename V>
 __device__ __forceinline__ V warp_sum(V v) {
@@ -100,39 +101,130 @@ __device__ __forceinline__ int sequence_of(const int32_t* off, int S, int T, int
   return lo;
 }
 
-// The softmax of a row held VPL values a lane: v becomes the probabilities (all
-// 0 for a row of -inf), and the row's logsumexp is returned (0 for such a row).
-template <int VPL>
-__device__ __forceinline__ float softmax_row(float (&v)[VPL]) {
-  float top = -INFINITY;
+// The same for the token of a warp, 32 offsets at a time.
+__device__ __forceinline__ int sequence_of_warp(const int32_t* off, int S, int T, int t, int lane) {
+  int lo = 0, hi = S;                            // the answer lies in [lo, hi]
+  while (lo < hi) {
+    const int step = (hi - lo + 31) / 32;
+    const unsigned m = __ballot_sync(kFull, offset_at(off, min(lo + lane * step + step, hi), T) > t);
+    if (m == 0) return hi;
+    const int first = __ffs(m) - 1;
+    hi = min(lo + first * step + step, hi) - 1;
+    lo += first * step;
+  }
+  return hi;
+}
+
+// The expert of value j on a lane.  VEC: four consecutive experts a lane, in
+// rounds of 128 (rows read and written 16 bytes at a time), else one in rounds
+// of 32.
+template <bool VEC>
+__device__ __forceinline__ int expert_of(int j, int lane) {
+  return VEC ? (j >> 2) * 128 + lane * 4 + (j & 3) : j * 32 + lane;
+}
+
+template <int VPL, bool VEC, typename V>
+__device__ __forceinline__ void load_row(const V* __restrict__ row, int E, int lane, V none, V (&v)[VPL]) {
+  if constexpr (VEC) {
 #pragma unroll
-  for (int j = 0; j < VPL; ++j) top = fmaxf(top, v[j]);
+    for (int j = 0; j < VPL; j += 4) {
+      const int e = expert_of<true>(j, lane);
+      const int4 x = e < E ? __ldg(reinterpret_cast<const int4*>(row + e)) : make_int4(0, 0, 0, 0);
+      const V* xs = reinterpret_cast<const V*>(&x);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[j + i] = e < E ? xs[i] : none;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) v[j] = j * 32 + lane < E ? __ldg(row + j * 32 + lane) : none;
+  }
+}
+
+// A row's maximum, 1 / sum of exp(l - max) and logsumexp; a row of nothing but
+// -inf has inv = 0 and lse = 0 (and top 0, so that exp(l - top) is 0).
+struct RowStat {
+  float top, inv, lse;
+};
+
+// The softmax of a row held VPL values a lane: v becomes the probabilities.
+template <int VPL>
+__device__ __forceinline__ RowStat softmax_row(float (&v)[VPL]) {
+  float top = v[0];
+#pragma unroll
+  for (int j = 1; j < VPL; ++j) top = fmaxf(top, v[j]);
   top = warp_max(top);
   const bool empty = top == -INFINITY;
+  if (empty) top = 0.f;
   float sum = 0.f;
 #pragma unroll
   for (int j = 0; j < VPL; ++j) {
-    v[j] = empty ? 0.f : expf(v[j] - top);
+    v[j] = expf(v[j] - top);
     sum += v[j];
   }
   sum = warp_sum(sum);
-  if (empty) return 0.f;
-  const float inv = 1.f / sum;
+  RowStat r;
+  r.top = top;
+  r.inv = empty ? 0.f : 1.f / sum;
+  r.lse = empty ? 0.f : top + logf(sum);
 #pragma unroll
-  for (int j = 0; j < VPL; ++j) v[j] *= inv;
-  return top + logf(sum);
+  for (int j = 0; j < VPL; ++j) v[j] *= r.inv;
+  return r;
 }
 
+// What a warp gathers over its tokens of one sequence.
 template <int VPL>
-__device__ __forceinline__ void load_row(const float* __restrict__ row, int E, int lane, float (&v)[VPL]) {
+struct Gathered {
+  float acc[VPL], z;
+  int n;
+};
+
+// Tokens lo + warp, lo + warp + warps, ... < hi: probabilities into registers,
+// pairs into the CTA's histogram.  The next token's row is in flight while one is
+// worked on.
+template <int VPL, bool VEC>
+__device__ __forceinline__ Gathered<VPL> gather_tokens(const float* __restrict__ logits, int E,
+                                                       const int32_t* __restrict__ idx, int k,
+                                                       const uint8_t* __restrict__ mask, int lo, int hi, int warp,
+                                                       int warps, int lane, int* hist, int32_t* status) {
+  Gathered<VPL> r;
+  r.z = 0.f;
+  r.n = 0;
 #pragma unroll
-  for (int j = 0; j < VPL; ++j) {
-    const int e = lane + 32 * j;
-    v[j] = e < E ? __ldg(row + e) : -INFINITY;
+  for (int j = 0; j < VPL; ++j) r.acc[j] = 0.f;
+  auto live = [&](int t) { return t < hi && (mask == nullptr || __ldg(mask + t) != 0); };
+  auto load = [&](int t, float (&v)[VPL], int& e) {
+    load_row<VPL, VEC>(logits + static_cast<size_t>(t) * E, E, lane, -INFINITY, v);
+    e = lane < k ? __ldg(idx + static_cast<size_t>(t) * k + lane) : 0;
+  };
+  float next[VPL];
+  int e_next = 0;
+  int t = lo + warp;
+  bool on = live(t);
+  if (on) load(t, next, e_next);
+  while (t < hi) {
+    float v[VPL];
+    const bool now = on;
+    const int e = e_next;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) v[j] = next[j];
+    t += warps;
+    on = live(t);
+    if (on) load(t, next, e_next);
+    if (!now) continue;
+    if (lane < k) {
+      if (e >= 0 && e < E) atomicAdd(&hist[e], 1);
+      else report(status, MOE_ERR_DEVICE);
+    }
+    const float lse = softmax_row<VPL>(v).lse;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) r.acc[j] += v[j];
+    r.z = fmaf(lse, lse, r.z);
+    ++r.n;
   }
+  return r;
 }
 
-template <int VPL>
+template <int VPL, bool VEC>
 __global__ void __launch_bounds__(kThreads) balance_partial_kernel(
     const float* __restrict__ logits, int T, int E, const int32_t* __restrict__ idx, int k,
     const int32_t* __restrict__ seq, int S, const uint8_t* __restrict__ mask, int tile_tokens, BalanceWs ws,
@@ -143,8 +235,10 @@ __global__ void __launch_bounds__(kThreads) balance_partial_kernel(
   __shared__ float wz[kWarps];
   __shared__ int wn[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (blockIdx.x == 0 && threadIdx.x == 0) *ws.ticket = 0;
   for (int e = threadIdx.x; e < E; e += kThreads) hist[e] = 0;
+  pdl_wait();
+  pdl_trigger();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *ws.ticket = 0;
   const int t0 = blockIdx.x * tile_tokens;
   const int t1 = min(T, t0 + tile_tokens);
   for (int s = seq == nullptr ? 0 : sequence_of(seq, S, T, t0); s < S; ++s) {
@@ -153,31 +247,14 @@ __global__ void __launch_bounds__(kThreads) balance_partial_kernel(
     const int lo = max(a, t0), hi = min(b, t1);
     if (lo >= hi) continue;
     __syncthreads();                                         // hist is clear, wsum may be written
-    float acc[VPL], z = 0.f;
-    int n = 0;
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) acc[j] = 0.f;
-    for (int t = lo + warp; t < hi; t += kWarps) {
-      if (mask != nullptr && __ldg(mask + t) == 0) continue;
-      float v[VPL];
-      load_row<VPL>(logits + static_cast<size_t>(t) * E, E, lane, v);
-      if (lane < k) {
-        const int e = __ldg(idx + static_cast<size_t>(t) * k + lane);
-        if (e >= 0 && e < E) atomicAdd(&hist[e], 1);
-        else report(status, MOE_ERR_DEVICE);
-      }
-      const float lse = softmax_row<VPL>(v);
-#pragma unroll
-      for (int j = 0; j < VPL; ++j) acc[j] += v[j];
-      z = fmaf(lse, lse, z);
-      ++n;
-    }
+    const Gathered<VPL> r =
+        gather_tokens<VPL, VEC>(logits, E, idx, k, mask, lo, hi, warp, kWarps, lane, hist, status);
 #pragma unroll
     for (int j = 0; j < VPL; ++j)
-      if (lane + 32 * j < E) wsum[warp * E + lane + 32 * j] = acc[j];
+      if (expert_of<VEC>(j, lane) < E) wsum[warp * E + expert_of<VEC>(j, lane)] = r.acc[j];
     if (lane == 0) {
-      wz[warp] = z;
-      wn[warp] = n;
+      wz[warp] = r.z;
+      wn[warp] = r.n;
     }
     __syncthreads();
     const size_t row = static_cast<size_t>(blockIdx.x) + s;
@@ -210,8 +287,81 @@ __device__ V block_sum(V v, V* sh) {
   if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
   __syncthreads();
   V s = 0;
-  for (int w = 0; w < kWarps; ++w) s += sh[w];
+  for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) s += sh[w];
   return s;
+}
+
+// One CTA does it all where the tokens are few: a second launch would cost more
+// than the whole sum.  Sequences one after the other; the loss and the factors,
+// which need the number of sequences with tokens, at the end.
+constexpr int kSmallTokens = 128;
+
+template <int VPL, bool VEC>
+__global__ void __launch_bounds__(VPL <= 8 ? 1024 : kThreads) balance_small_kernel(
+    const float* __restrict__ logits, int T, int E, const int32_t* __restrict__ idx, int k,
+    const int32_t* __restrict__ seq, int S, const uint8_t* __restrict__ mask, int32_t* __restrict__ tokens,
+    float* __restrict__ loss, int32_t* __restrict__ counts, float* __restrict__ prob, float* __restrict__ coef,
+    int32_t* status) {
+  extern __shared__ float smem[];
+  const int threads = blockDim.x, warps = threads >> 5;
+  float* wsum = smem;                                        // [warps][E]
+  int* hist = reinterpret_cast<int*>(smem + warps * E);      // [E]
+  __shared__ float wz[32];
+  __shared__ int wn[32];
+  __shared__ double shd[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int e = threadIdx.x; e < E; e += threads) hist[e] = 0;
+  pdl_wait();
+  pdl_trigger();
+  double ball = 0, zall = 0;
+  int some = 0, all = 0;
+  for (int s = 0; s < S; ++s) {
+    int a = 0, b = T;
+    if (seq != nullptr) {
+      a = offset_at(seq, s, T);
+      b = offset_at(seq, s + 1, T);
+      if (threadIdx.x == 0 && (a > b || a != __ldg(seq + s) || b != __ldg(seq + s + 1))) report(status, MOE_ERR_DEVICE);
+    }
+    __syncthreads();                                         // hist is clear, wsum may be written
+    const Gathered<VPL> r = gather_tokens<VPL, VEC>(logits, E, idx, k, mask, a, b, warp, warps, lane, hist, status);
+#pragma unroll
+    for (int j = 0; j < VPL; ++j)
+      if (expert_of<VEC>(j, lane) < E) wsum[warp * E + expert_of<VEC>(j, lane)] = r.acc[j];
+    if (lane == 0) {
+      wz[warp] = r.z;
+      wn[warp] = r.n;
+    }
+    __syncthreads();
+    double z = 0, q = 0;
+    int n = 0;
+    for (int w = 0; w < warps; ++w) {
+      z += wz[w];
+      n += wn[w];
+    }
+    for (int e = threadIdx.x; e < E; e += threads) {
+      double p = 0;
+      for (int w = 0; w < warps; ++w) p += wsum[w * E + e];
+      const int c = hist[e];
+      hist[e] = 0;
+      counts[static_cast<size_t>(s) * E + e] = c;
+      prob[static_cast<size_t>(s) * E + e] = n > 0 ? static_cast<float>(p / n) : 0.f;
+      q += p * c;
+    }
+    q = block_sum(q, shd);
+    if (threadIdx.x == 0) tokens[s] = n;
+    if (n > 0) ball += q * E / (static_cast<double>(k) * n * n);
+    zall += z;
+    some += n > 0;
+    all += n;
+  }
+  if (threadIdx.x != 0) return;
+  for (int s = 0; s < S; ++s) {
+    const int n = tokens[s];
+    coef[s] = n > 0 ? static_cast<float>(E / (static_cast<double>(k) * n * n * some)) : 0.f;
+  }
+  coef[S] = 1.f / static_cast<float>(all > 0 ? all : 1);
+  loss[0] = some > 0 ? static_cast<float>(ball / some) : 0.f;
+  loss[1] = all > 0 ? static_cast<float>(zall / all) : 0.f;
 }
 
 __global__ void __launch_bounds__(kThreads) balance_finish_kernel(
@@ -225,6 +375,8 @@ __global__ void __launch_bounds__(kThreads) balance_finish_kernel(
   __shared__ bool last;
   const int s = blockIdx.x, eb = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int e = eb * 32 + lane;
+  pdl_wait();
+  pdl_trigger();
   int a = 0, b = T;
   if (seq != nullptr) {
     a = offset_at(seq, s, T);
@@ -308,7 +460,7 @@ __global__ void __launch_bounds__(kThreads) balance_finish_kernel(
   }
 }
 
-template <int VPL>
+template <int VPL, bool VEC>
 __global__ void __launch_bounds__(kThreads) router_backward_kernel(
     const float* __restrict__ logits, int T, int E, const int32_t* __restrict__ idx, const float* __restrict__ gate,
     const float* __restrict__ dgate, int k, const int32_t* __restrict__ seq, int S, const uint8_t* __restrict__ mask,
@@ -316,6 +468,8 @@ __global__ void __launch_bounds__(kThreads) router_backward_kernel(
     float* __restrict__ dlogits, int32_t* status) {
   const int lane = threadIdx.x & 31;
   const int t = static_cast<int>((blockIdx.x * static_cast<long long>(kThreads) + threadIdx.x) >> 5);
+  pdl_wait();
+  pdl_trigger();
   if (t >= T) return;
   float d[VPL];
 #pragma unroll
@@ -323,47 +477,72 @@ __global__ void __launch_bounds__(kThreads) router_backward_kernel(
   int s = 0;
   bool live = mask == nullptr || __ldg(mask + t) != 0;
   if (live && seq != nullptr) {
-    s = sequence_of(seq, S, T, t);
+    s = sequence_of_warp(seq, S, T, t, lane);
     live = s < S && offset_at(seq, s, T) <= t;
   }
-  if (live && dloss != nullptr) {
-    load_row<VPL>(logits + static_cast<size_t>(t) * E, E, lane, d);
-    const float lse = softmax_row<VPL>(d);
-    const float cb = __ldg(dloss) * __ldg(coef + s), cz = 2.f * __ldg(dloss + 1) * __ldg(coef + S) * lse;
-    const int32_t* crow = counts + static_cast<size_t>(s) * E;
-    float f[VPL], dot = 0.f;
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) {
-      const int e = lane + 32 * j;
-      f[j] = e < E ? static_cast<float>(__ldg(crow + e)) : 0.f;
-      dot = fmaf(f[j], d[j], dot);
-    }
-    dot = warp_sum(dot);
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) d[j] *= fmaf(cb, f[j] - dot, cz);
-  }
-  if (live && dgate != nullptr) {
-    const bool on = lane < k;
+  // the pairs of the token, one a lane
+  const bool gates = live && dgate != nullptr, on = gates && lane < k;
+  float v = 0.f;
+  int e = -1;
+  if (gates) {
     const size_t p = static_cast<size_t>(t) * k + lane;
     const float g = on ? __ldg(gate + p) : 0.f, dg = on ? __ldg(dgate + p) : 0.f;
-    int e = on ? __ldg(idx + p) : -1;
+    if (on) e = __ldg(idx + p);
     if (on && (e < 0 || e >= E)) {
       report(status, MOE_ERR_DEVICE);
       e = -1;
     }
-    const float v = g * (dg - warp_sum(on ? g * dg : 0.f));
-    for (int i = 0; i < k; ++i) {
-      const int ei = __shfl_sync(kFull, e, i);
-      const float vi = __shfl_sync(kFull, v, i);
+    v = g * (dg - warp_sum(g * dg));
+  }
+  const float* lrow = logits + static_cast<size_t>(t) * E;
+  const int32_t* crow = counts + static_cast<size_t>(s) * E;
+  RowStat st{0.f, 0.f, 0.f};
+  float cb = 0.f, cz = 0.f, dot = 0.f;
+  const bool losses = live && dloss != nullptr;
+  if (losses) {
+    int32_t f[VPL];
+    load_row<VPL, VEC>(lrow, E, lane, -INFINITY, d);
+    load_row<VPL, VEC>(crow, E, lane, 0, f);
+    cb = __ldg(dloss) * __ldg(coef + s);
+    cz = 2.f * __ldg(dloss + 1) * __ldg(coef + S);
+    st = softmax_row<VPL>(d);
+    cz *= st.lse;
 #pragma unroll
-      for (int j = 0; j < VPL; ++j)
-        if (lane + 32 * j == ei) d[j] += vi;
-    }
+    for (int j = 0; j < VPL; ++j) dot = fmaf(static_cast<float>(f[j]), d[j], dot);
+    dot = warp_sum(dot);
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) d[j] *= fmaf(cb, static_cast<float>(f[j]) - dot, cz);
   }
   float* row = dlogits + static_cast<size_t>(t) * E;
+  if constexpr (VEC) {
 #pragma unroll
-  for (int j = 0; j < VPL; ++j)
-    if (lane + 32 * j < E) row[lane + 32 * j] = d[j];
+    for (int j = 0; j < VPL; j += 4)
+      if (expert_of<true>(j, lane) < E)
+        *reinterpret_cast<float4*>(row + expert_of<true>(j, lane)) = make_float4(d[j], d[j + 1], d[j + 2], d[j + 3]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < VPL; ++j)
+      if (j * 32 + lane < E) row[j * 32 + lane] = d[j];
+  }
+  if (!gates) return;
+  // The chosen experts' values again, by their pairs' lanes, with the gate term:
+  // k values to form and store over those above instead of a search for each of
+  // the k experts' owners.  An id that occurs twice is summed by its first lane.
+  const unsigned same = __match_any_sync(kFull, e);
+  float sum = v;
+  if (__any_sync(kFull, e >= 0 && __popc(same) > 1)) {
+    sum = 0.f;
+    for (int i = 0; i < k; ++i) {
+      const float vi = __shfl_sync(kFull, v, i);
+      if (same >> i & 1u) sum += vi;
+    }
+  }
+  __syncwarp();
+  if (e >= 0 && __ffs(same) - 1 == lane) {
+    float x = 0.f;
+    if (losses) x = expf(__ldg(lrow + e) - st.top) * st.inv * fmaf(cb, static_cast<float>(__ldg(crow + e)) - dot, cz);
+    row[e] = x + sum;
+  }
 }
 
 moe_status check_sequences(int T, int E, int k, const int32_t* seq, int S) {
@@ -377,15 +556,18 @@ moe_status check_sequences(int T, int E, int k, const int32_t* seq, int S) {
   return MOE_OK;
 }
 
-// f(VPL constant): the number of experts a lane holds for E experts.
+// f(VPL, VEC): the number of experts a lane holds for E experts, and whether rows
+// are moved 16 bytes at a time.
 template <typename F>
-cudaError_t with_vpl(int E, F f) {
-  if (E <= 32) return f(std::integral_constant<int, 1>());
-  if (E <= 64) return f(std::integral_constant<int, 2>());
-  if (E <= 128) return f(std::integral_constant<int, 4>());
-  if (E <= 256) return f(std::integral_constant<int, 8>());
-  if (E <= 512) return f(std::integral_constant<int, 16>());
-  return f(std::integral_constant<int, 32>());
+cudaError_t with_row(int E, bool vec, F f) {
+  const std::true_type yes;
+  const std::false_type no;
+  if (E <= 32) return f(std::integral_constant<int, 1>(), no);
+  if (E <= 64) return f(std::integral_constant<int, 2>(), no);
+  if (E <= 128) return vec ? f(std::integral_constant<int, 4>(), yes) : f(std::integral_constant<int, 4>(), no);
+  if (E <= 256) return vec ? f(std::integral_constant<int, 8>(), yes) : f(std::integral_constant<int, 8>(), no);
+  if (E <= 512) return vec ? f(std::integral_constant<int, 16>(), yes) : f(std::integral_constant<int, 16>(), no);
+  return vec ? f(std::integral_constant<int, 32>(), yes) : f(std::integral_constant<int, 32>(), no);
 }
 
 }  // namespace
@@ -425,16 +607,26 @@ extern "C" moe_status moe_balance_loss(const float* logits, int T, int E, const 
   ws.sn = reinterpret_cast<int32_t*>(w + L.sn);
   ws.sz = reinterpret_cast<double*>(w + L.sz);
   ws.ticket = reinterpret_cast<unsigned*>(w + L.ticket);
+  const bool vec = E % 4 == 0 && aligned(logits, 16);
+  if (T <= kSmallTokens && S <= kSmallTokens) {
+    const int warps = E <= 256 ? 32 : kWarps;   // registers: VPL <= 8 values a lane, or more
+    const cudaError_t err = with_row(E, vec, [&](auto vpl, auto v) {
+      return launch_pdl(balance_small_kernel<decltype(vpl)::value, decltype(v)::value>, dim3(1), dim3(warps * 32),
+                        static_cast<size_t>(warps + 1) * E * 4, stream, logits, T, E, idx, k, seq_offsets, S, mask,
+                        ws.sn, loss, counts, prob, coef, dev_status);
+    });
+    if (err != cudaSuccess) return fail(MOE_ERR_CUDA, "balance_small launch: %s", cudaGetErrorString(err));
+    MOE_LAUNCH_CHECK("balance_small_kernel");
+    return MOE_OK;
+  }
   const size_t smem = static_cast<size_t>(kWarps + 1) * E * 4;     // <= 36 KB
-  const cudaError_t err = with_vpl(E, [&](auto vpl) {
-    balance_partial_kernel<decltype(vpl)::value><<<L.tiles, kThreads, smem, stream>>>(
-        logits, T, E, idx, k, seq_offsets, S, mask, L.tile_tokens, ws, dev_status);
-    return cudaGetLastError();
+  const cudaError_t err = with_row(E, vec, [&](auto vpl, auto v) {
+    return launch_pdl(balance_partial_kernel<decltype(vpl)::value, decltype(v)::value>, dim3(L.tiles), dim3(kThreads),
+                      smem, stream, logits, T, E, idx, k, seq_offsets, S, mask, L.tile_tokens, ws, dev_status);
   });
   if (err != cudaSuccess) return fail(MOE_ERR_CUDA, "balance_partial launch: %s", cudaGetErrorString(err));
-  balance_finish_kernel<<<dim3(S, L.eblocks), kThreads, 0, stream>>>(T, E, k, seq_offsets, S, L.tile_tokens,
-                                                                     L.eblocks, ws, loss, counts, prob, coef,
-                                                                     dev_status);
+  MOE_CUDA_TRY(launch_pdl(balance_finish_kernel, dim3(S, L.eblocks), dim3(kThreads), 0, stream, T, E, k, seq_offsets, S,
+                          L.tile_tokens, L.eblocks, ws, loss, counts, prob, coef, dev_status));
   MOE_LAUNCH_CHECK("balance_finish_kernel");
   return MOE_OK;
 }
@@ -456,10 +648,11 @@ extern "C" moe_status moe_router_backward(const float* logits, int T, int E, con
   st = current_device(&dev);
   if (st != MOE_OK) return st;
   const int blocks = (T + kWarps - 1) / kWarps;
-  const cudaError_t err = with_vpl(E, [&](auto vpl) {
-    router_backward_kernel<decltype(vpl)::value><<<blocks, kThreads, 0, stream>>>(
-        logits, T, E, idx, gate, dgate, k, seq_offsets, S, mask, counts, coef, dloss, dlogits, dev_status);
-    return cudaGetLastError();
+  const bool vec = E % 4 == 0 && aligned(logits, 16) && aligned(dlogits, 16) && aligned(counts, 16);
+  const cudaError_t err = with_row(E, vec, [&](auto vpl, auto v) {
+    return launch_pdl(router_backward_kernel<decltype(vpl)::value, decltype(v)::value>, dim3(blocks), dim3(kThreads), 0,
+                      stream, logits, T, E, idx, gate, dgate, k, seq_offsets, S, mask, counts, coef, dloss, dlogits,
+                      dev_status);
   });
   if (err != cudaSuccess) return fail(MOE_ERR_CUDA, "router_backward launch: %s", cudaGetErrorString(err));
   return MOE_OK;
