@@ -140,13 +140,24 @@ __device__ __forceinline__ void load_row(const V* __restrict__ row, int E, int l
   }
 }
 
+// exp(l - top) through 2^x.  The rounded product is off by up to |x| 2^-24, so a
+// value is off by |l - top| 2^-24 of itself: e^-16 (a value that adds 1e-7 to a
+// sum) by 2^-20, and the large ones that make the sums by a few 2^-24.  (Values
+// below 2^-126 are 0.)
+__device__ __forceinline__ float exp_below(float l, float top) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"((l - top) * 1.4426950408889634f));
+  return r;
+}
+
 // A row's maximum, 1 / sum of exp(l - max) and logsumexp; a row of nothing but
 // -inf has inv = 0 and lse = 0 (and top 0, so that exp(l - top) is 0).
 struct RowStat {
   float top, inv, lse;
 };
 
-// The softmax of a row held VPL values a lane: v becomes the probabilities.
+// The softmax of a row held VPL values a lane: v becomes exp(l - max), the
+// probabilities over inv.
 template <int VPL>
 __device__ __forceinline__ RowStat softmax_row(float (&v)[VPL]) {
   float top = v[0];
@@ -158,16 +169,14 @@ __device__ __forceinline__ RowStat softmax_row(float (&v)[VPL]) {
   float sum = 0.f;
 #pragma unroll
   for (int j = 0; j < VPL; ++j) {
-    v[j] = expf(v[j] - top);
+    v[j] = exp_below(v[j], top);
     sum += v[j];
   }
   sum = warp_sum(sum);
   RowStat r;
   r.top = top;
-  r.inv = empty ? 0.f : 1.f / sum;
-  r.lse = empty ? 0.f : top + logf(sum);
-#pragma unroll
-  for (int j = 0; j < VPL; ++j) v[j] *= r.inv;
+  r.inv = empty ? 0.f : __fdividef(1.f, sum);       // 1 <= sum <= E: within 2^-23 and 2^-21
+  r.lse = empty ? 0.f : top + __logf(sum);
   return r;
 }
 
@@ -178,48 +187,50 @@ struct Gathered {
   int n;
 };
 
-// Tokens lo + warp, lo + warp + warps, ... < hi: probabilities into registers,
-// pairs into the CTA's histogram.  The next token's row is in flight while one is
-// worked on.
+// The tokens lo <= t < hi that count: probabilities into registers, pairs into the
+// CTA's histogram.  A warp takes every `warps`-th group of G tokens, finds by a
+// ballot which of them count, and works on two at a time (whose rows are in
+// flight together; an odd last one stands in for its missing partner, at weight 0).
 template <int VPL, bool VEC>
 __device__ __forceinline__ Gathered<VPL> gather_tokens(const float* __restrict__ logits, int E,
                                                        const int32_t* __restrict__ idx, int k,
                                                        const uint8_t* __restrict__ mask, int lo, int hi, int warp,
                                                        int warps, int lane, int* hist, int32_t* status) {
+  constexpr int R = VPL <= 8 ? 2 : 1;            // rows in flight: registers
   Gathered<VPL> r;
   r.z = 0.f;
   r.n = 0;
 #pragma unroll
   for (int j = 0; j < VPL; ++j) r.acc[j] = 0.f;
-  auto live = [&](int t) { return t < hi && (mask == nullptr || __ldg(mask + t) != 0); };
-  auto load = [&](int t, float (&v)[VPL], int& e) {
-    load_row<VPL, VEC>(logits + static_cast<size_t>(t) * E, E, lane, -INFINITY, v);
-    e = lane < k ? __ldg(idx + static_cast<size_t>(t) * k + lane) : 0;
-  };
-  float next[VPL];
-  int e_next = 0;
-  int t = lo + warp;
-  bool on = live(t);
-  if (on) load(t, next, e_next);
-  while (t < hi) {
-    float v[VPL];
-    const bool now = on;
-    const int e = e_next;
+  const int G = max(1, min(32, (hi - lo + warps - 1) / warps));
+  for (int t0 = lo + warp * G; t0 < hi; t0 += warps * G) {
+    const int mine = t0 + lane;
+    unsigned m = __ballot_sync(kFull, lane < G && mine < hi && (mask == nullptr || __ldg(mask + mine) != 0));
+    r.n += __popc(m);
+    while (m != 0) {
+      float v[R][VPL], w[R];
+      int e[R], t = 0;
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) v[j] = next[j];
-    t += warps;
-    on = live(t);
-    if (on) load(t, next, e_next);
-    if (!now) continue;
-    if (lane < k) {
-      if (e >= 0 && e < E) atomicAdd(&hist[e], 1);
-      else report(status, MOE_ERR_DEVICE);
+      for (int i = 0; i < R; ++i) {
+        w[i] = m != 0 ? 1.f : 0.f;
+        if (m != 0) t = t0 + __ffs(m) - 1;
+        m &= m - 1;
+        load_row<VPL, VEC>(logits + static_cast<size_t>(t) * E, E, lane, -INFINITY, v[i]);
+        e[i] = lane < k ? __ldg(idx + static_cast<size_t>(t) * k + lane) : 0;
+      }
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        if (lane < k && w[i] != 0.f) {
+          if (e[i] >= 0 && e[i] < E) atomicAdd(&hist[e[i]], 1);
+          else report(status, MOE_ERR_DEVICE);
+        }
+        const RowStat st = softmax_row<VPL>(v[i]);
+        const float inv = w[i] * st.inv;
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) r.acc[j] = fmaf(v[i][j], inv, r.acc[j]);
+        r.z = fmaf(w[i] * st.lse, st.lse, r.z);
+      }
     }
-    const float lse = softmax_row<VPL>(v).lse;
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) r.acc[j] += v[j];
-    r.z = fmaf(lse, lse, r.z);
-    ++r.n;
   }
   return r;
 }
@@ -368,10 +379,9 @@ __global__ void __launch_bounds__(kThreads) balance_finish_kernel(
     int T, int E, int k, const int32_t* __restrict__ seq, int S, int tile_tokens, int eblocks, BalanceWs ws,
     float* __restrict__ loss, int32_t* __restrict__ counts, float* __restrict__ prob, float* __restrict__ coef,
     int32_t* status) {
-  __shared__ double shd[kWarps];
-  __shared__ int shi[kWarps];
   __shared__ double wp[kWarps][32];
   __shared__ int wc[kWarps][32];
+  __shared__ double wall[kWarps][4];
   __shared__ bool last;
   const int s = blockIdx.x, eb = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int e = eb * 32 + lane;
@@ -387,25 +397,24 @@ __global__ void __launch_bounds__(kThreads) balance_finish_kernel(
   // the rows of this sequence (none if it is empty)
   const size_t r0 = static_cast<size_t>(a / tile_tokens) + s;
   const int rows = a < b ? (b - 1) / tile_tokens - a / tile_tokens + 1 : 0;
-  int n = 0;
-  double z = 0;
-  for (int r = threadIdx.x; r < rows; r += kThreads) {
-    n += ws.n[r0 + r];
-    z += ws.z[r0 + r];
-  }
-  n = block_sum(n, shi);
-  z = block_sum(z, shd);
-  double p = 0;
-  int c = 0;
+  double p = 0, z = 0;
+  int c = 0, n = 0;
   if (e < E)
+#pragma unroll 4
     for (int r = warp; r < rows; r += kWarps) {
       p += ws.p[(r0 + r) * E + e];
       c += ws.c[(r0 + r) * E + e];
+    }
+  if (warp == 0)
+    for (int r = lane; r < rows; r += 32) {
+      n += ws.n[r0 + r];
+      z += ws.z[r0 + r];
     }
   wp[warp][lane] = p;
   wc[warp][lane] = c;
   __syncthreads();
   if (warp == 0) {
+    n = warp_sum(n);
     p = 0;
     c = 0;
     for (int w = 0; w < kWarps; ++w) {
@@ -417,6 +426,7 @@ __global__ void __launch_bounds__(kThreads) balance_finish_kernel(
       prob[static_cast<size_t>(s) * E + e] = n > 0 ? static_cast<float>(p / n) : 0.f;
     }
     const double q = warp_sum(e < E ? p * c : 0.0);
+    if (eb == 0) z = warp_sum(z);
     if (lane == 0) {
       ws.q[static_cast<size_t>(s) * eblocks + eb] = q;
       if (eb == 0) {
@@ -430,118 +440,144 @@ __global__ void __launch_bounds__(kThreads) balance_finish_kernel(
   __syncthreads();
   if (!last) return;
   __threadfence();
-  // the last CTA: every other one's sums are visible
-  int some = 0;
-  long long total = 0;
-  double zall = 0, ball = 0;
+  // The last CTA: every other one's sums are visible.  all[]: sequences with
+  // tokens, tokens (whole numbers, exact in 64 bits), lse^2, balance terms.
+  double all[4] = {0, 0, 0, 0};
   for (int i = threadIdx.x; i < S; i += kThreads) {
     const int ni = __ldcg(ws.sn + i);
-    some += ni > 0;
-    total += ni;
-    zall += __ldcg(ws.sz + i);
-    if (ni > 0) {
-      double q = 0;
-      for (int j = 0; j < eblocks; ++j) q += __ldcg(ws.q + static_cast<size_t>(i) * eblocks + j);
-      ball += q * E / (static_cast<double>(k) * ni * ni);
-    }
+    double q = 0;
+    for (int j = 0; j < eblocks; ++j) q += __ldcg(ws.q + static_cast<size_t>(i) * eblocks + j);
+    all[0] += ni > 0;
+    all[1] += ni;
+    all[2] += __ldcg(ws.sz + i);
+    if (ni > 0) all[3] += q * E / (static_cast<double>(k) * ni * ni);
   }
-  some = block_sum(some, shi);
-  const int all = block_sum(static_cast<int>(total), shi);     // <= T
-  zall = block_sum(zall, shd);
-  ball = block_sum(ball, shd);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    all[i] = warp_sum(all[i]);
+    if (lane == 0) wall[warp][i] = all[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    all[i] = 0;
+    for (int w = 0; w < kWarps; ++w) all[i] += wall[w][i];
+  }
   for (int i = threadIdx.x; i < S; i += kThreads) {
     const int ni = __ldcg(ws.sn + i);
-    coef[i] = ni > 0 ? static_cast<float>(E / (static_cast<double>(k) * ni * ni * some)) : 0.f;
+    coef[i] = ni > 0 ? static_cast<float>(E / (static_cast<double>(k) * ni * ni * all[0])) : 0.f;
   }
   if (threadIdx.x == 0) {
-    coef[S] = 1.f / static_cast<float>(all > 0 ? all : 1);
-    loss[0] = some > 0 ? static_cast<float>(ball / some) : 0.f;
-    loss[1] = all > 0 ? static_cast<float>(zall / all) : 0.f;
+    coef[S] = static_cast<float>(1.0 / (all[1] > 0 ? all[1] : 1.0));
+    loss[0] = all[0] > 0 ? static_cast<float>(all[3] / all[0]) : 0.f;
+    loss[1] = all[1] > 0 ? static_cast<float>(all[2] / all[1]) : 0.f;
   }
 }
 
+// `rows` consecutive tokens a warp.
 template <int VPL, bool VEC>
 __global__ void __launch_bounds__(kThreads) router_backward_kernel(
     const float* __restrict__ logits, int T, int E, const int32_t* __restrict__ idx, const float* __restrict__ gate,
     const float* __restrict__ dgate, int k, const int32_t* __restrict__ seq, int S, const uint8_t* __restrict__ mask,
     const int32_t* __restrict__ counts, const float* __restrict__ coef, const float* __restrict__ dloss,
-    float* __restrict__ dlogits, int32_t* status) {
+    float* __restrict__ dlogits, int rows, int32_t* status) {
   const int lane = threadIdx.x & 31;
-  const int t = static_cast<int>((blockIdx.x * static_cast<long long>(kThreads) + threadIdx.x) >> 5);
+  const long long first = ((blockIdx.x * static_cast<long long>(kThreads) + threadIdx.x) >> 5) * rows;
   pdl_wait();
   pdl_trigger();
-  if (t >= T) return;
-  float d[VPL];
-#pragma unroll
-  for (int j = 0; j < VPL; ++j) d[j] = 0.f;
-  int s = 0;
-  bool live = mask == nullptr || __ldg(mask + t) != 0;
-  if (live && seq != nullptr) {
-    s = sequence_of_warp(seq, S, T, t, lane);
-    live = s < S && offset_at(seq, s, T) <= t;
+  if (first >= T) return;
+  const int end = static_cast<int>(min(first + rows, static_cast<long long>(T)));
+  const bool with_loss = dloss != nullptr, with_gates = dgate != nullptr, on = lane < k;
+  const float dl = with_loss ? __ldg(dloss) : 0.f, dz = with_loss ? 2.f * __ldg(dloss + 1) * __ldg(coef + S) : 0.f;
+  int s = 0, seq_begin = 0, seq_end = 0;          // the sequence that ends first behind the token
+  float cb0 = 0.f;
+  if (seq == nullptr) {
+    seq_end = T;
+    if (with_loss) cb0 = dl * __ldg(coef);
   }
-  // the pairs of the token, one a lane
-  const bool gates = live && dgate != nullptr, on = gates && lane < k;
-  float v = 0.f;
-  int e = -1;
-  if (gates) {
-    const size_t p = static_cast<size_t>(t) * k + lane;
-    const float g = on ? __ldg(gate + p) : 0.f, dg = on ? __ldg(dgate + p) : 0.f;
-    if (on) e = __ldg(idx + p);
-    if (on && (e < 0 || e >= E)) {
-      report(status, MOE_ERR_DEVICE);
-      e = -1;
+  const int t0 = static_cast<int>(first);
+  const unsigned counted =
+      mask == nullptr ? ~0u : __ballot_sync(kFull, t0 + lane < end && __ldg(mask + t0 + lane) != 0);   // rows <= 32
+  for (int t = t0; t < end; ++t) {
+    float* row = dlogits + static_cast<size_t>(t) * E;
+    bool live = counted >> (t - t0) & 1u;
+    if (t >= seq_end) {                           // seq != nullptr
+      s = sequence_of_warp(seq, S, T, t, lane);
+      seq_begin = s < S ? offset_at(seq, s, T) : T;
+      seq_end = s < S ? offset_at(seq, s + 1, T) : T;
+      if (with_loss && s < S) cb0 = dl * __ldg(coef + s);
     }
-    v = g * (dg - warp_sum(g * dg));
-  }
-  const float* lrow = logits + static_cast<size_t>(t) * E;
-  const int32_t* crow = counts + static_cast<size_t>(s) * E;
-  RowStat st{0.f, 0.f, 0.f};
-  float cb = 0.f, cz = 0.f, dot = 0.f;
-  const bool losses = live && dloss != nullptr;
-  if (losses) {
-    int32_t f[VPL];
-    load_row<VPL, VEC>(lrow, E, lane, -INFINITY, d);
-    load_row<VPL, VEC>(crow, E, lane, 0, f);
-    cb = __ldg(dloss) * __ldg(coef + s);
-    cz = 2.f * __ldg(dloss + 1) * __ldg(coef + S);
-    st = softmax_row<VPL>(d);
-    cz *= st.lse;
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) dot = fmaf(static_cast<float>(f[j]), d[j], dot);
-    dot = warp_sum(dot);
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) d[j] *= fmaf(cb, static_cast<float>(f[j]) - dot, cz);
-  }
-  float* row = dlogits + static_cast<size_t>(t) * E;
-  if constexpr (VEC) {
-#pragma unroll
-    for (int j = 0; j < VPL; j += 4)
-      if (expert_of<true>(j, lane) < E)
-        *reinterpret_cast<float4*>(row + expert_of<true>(j, lane)) = make_float4(d[j], d[j + 1], d[j + 2], d[j + 3]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < VPL; ++j)
-      if (j * 32 + lane < E) row[j * 32 + lane] = d[j];
-  }
-  if (!gates) return;
-  // The chosen experts' values again, by their pairs' lanes, with the gate term:
-  // k values to form and store over those above instead of a search for each of
-  // the k experts' owners.  An id that occurs twice is summed by its first lane.
-  const unsigned same = __match_any_sync(kFull, e);
-  float sum = v;
-  if (__any_sync(kFull, e >= 0 && __popc(same) > 1)) {
-    sum = 0.f;
-    for (int i = 0; i < k; ++i) {
-      const float vi = __shfl_sync(kFull, v, i);
-      if (same >> i & 1u) sum += vi;
+    live = live && t >= seq_begin;
+    if (!live) {
+      for (int e = lane; e < E; e += 32) row[e] = 0.f;
+      continue;
     }
-  }
-  __syncwarp();
-  if (e >= 0 && __ffs(same) - 1 == lane) {
-    float x = 0.f;
-    if (losses) x = expf(__ldg(lrow + e) - st.top) * st.inv * fmaf(cb, static_cast<float>(__ldg(crow + e)) - dot, cz);
-    row[e] = x + sum;
+    const float* lrow = logits + static_cast<size_t>(t) * E;
+    const int32_t* crow = counts + static_cast<size_t>(s) * E;
+    float d[VPL];
+    // the pairs of the token, one a lane
+    float g = 0.f, dg = 0.f;
+    int e = -1;
+    if (with_loss) load_row<VPL, VEC>(lrow, E, lane, -INFINITY, d);
+    if (with_gates && on) {
+      const size_t p = static_cast<size_t>(t) * k + lane;
+      g = __ldg(gate + p);
+      dg = __ldg(dgate + p);
+      e = __ldg(idx + p);
+      if (e < 0 || e >= E) {
+        report(status, MOE_ERR_DEVICE);
+        e = -1;
+      }
+    }
+    RowStat st{0.f, 0.f, 0.f};
+    float dot = 0.f, cz = 0.f;
+    if (with_loss) {
+      int32_t f[VPL];
+      load_row<VPL, VEC>(crow, E, lane, 0, f);
+      st = softmax_row<VPL>(d);
+      cz = dz * st.lse;
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) dot = fmaf(static_cast<float>(f[j]), d[j], dot);
+      dot = warp_sum(dot) * st.inv;
+      // p (cb (f - dot) + cz) with p = d inv
+      const float cb = cb0 * st.inv, c0 = cz * st.inv - cb * dot;
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) d[j] *= fmaf(cb, static_cast<float>(f[j]), c0);
+    } else {
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) d[j] = 0.f;
+    }
+    if constexpr (VEC) {
+#pragma unroll
+      for (int j = 0; j < VPL; j += 4)
+        if (expert_of<true>(j, lane) < E)
+          *reinterpret_cast<float4*>(row + expert_of<true>(j, lane)) = make_float4(d[j], d[j + 1], d[j + 2], d[j + 3]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < VPL; ++j)
+        if (j * 32 + lane < E) row[j * 32 + lane] = d[j];
+    }
+    if (!with_gates) continue;
+    // The chosen experts' values again, by their pairs' lanes, with the gate term:
+    // k values to form and store over those above instead of a search for each of
+    // the k experts' owners.  An id that occurs twice is summed by its first lane.
+    const float v = g * (dg - warp_sum(g * dg));
+    const unsigned same = __match_any_sync(kFull, e);
+    float sum = v;
+    if (__any_sync(kFull, e >= 0 && __popc(same) > 1)) {
+      sum = 0.f;
+      for (int i = 0; i < k; ++i) {
+        const float vi = __shfl_sync(kFull, v, i);
+        if (same >> i & 1u) sum += vi;
+      }
+    }
+    __syncwarp();
+    if (e >= 0 && __ffs(same) - 1 == lane) {
+      float x = 0.f;
+      if (with_loss)
+        x = exp_below(__ldg(lrow + e), st.top) * st.inv * fmaf(cb0, static_cast<float>(__ldg(crow + e)) - dot, cz);
+      row[e] = x + sum;
+    }
   }
 }
 
@@ -647,12 +683,16 @@ extern "C" moe_status moe_router_backward(const float* logits, int T, int E, con
   DeviceInfo dev;
   st = current_device(&dev);
   if (st != MOE_OK) return st;
-  const int blocks = (T + kWarps - 1) / kWarps;
+  // One token a warp until every warp slot of the SMs (about 40 each) has had one,
+  // then up to 4: what a warp reads once counts for more rows.
+  int rows = T / (40 * dev.sm_count);
+  rows = rows < 1 ? 1 : rows > 4 ? 4 : rows;
+  const int blocks = (T + kWarps * rows - 1) / (kWarps * rows);
   const bool vec = E % 4 == 0 && aligned(logits, 16) && aligned(dlogits, 16) && aligned(counts, 16);
   const cudaError_t err = with_row(E, vec, [&](auto vpl, auto v) {
     return launch_pdl(router_backward_kernel<decltype(vpl)::value, decltype(v)::value>, dim3(blocks), dim3(kThreads), 0,
                       stream, logits, T, E, idx, gate, dgate, k, seq_offsets, S, mask, counts, coef, dloss, dlogits,
-                      dev_status);
+                      rows, dev_status);
   });
   if (err != cudaSuccess) return fail(MOE_ERR_CUDA, "router_backward launch: %s", cudaGetErrorString(err));
   return MOE_OK;
