@@ -79,7 +79,7 @@ _SIGS = {
     "moe_cache_query": (_I, [_P, _P, _P, _P]),
     "moe_cache_destroy": (_I, [_P]),
     "moe_check_status": (_I, [_P, _P]),
-    "moe_linear_w4": (_I, [moe_linear_shape, _P, _P, _P, ctypes.c_float, _P, _I, _I64, _I, _P, _I, _I64, _I, _P]),
+    "moe_linear_w4": (_I, [moe_linear_shape, _P, _P, _P, ctypes.c_float, _P, _I, _I64, _I, _P, _I, _I64, _I, _P, _P]),
     "moe_balance_loss_workspace_bytes": (_SZ, [_I, _I, _I]),
     "moe_balance_loss": (_I, [_P, _I, _I, _P, _I, _P, _I, _P, _P, _P, _P, _P, _P, _SZ, _P, _P]),
     "moe_router_backward": (_I, [_P, _I, _I, _P, _P, _P, _I, _P, _I, _P, _P, _P, _P, _P, _P, _P]),
@@ -314,7 +314,7 @@ def _done(status: int):
 
 
 def moe_linear_w4(x, codes, scales, out, fmt="int4", group: int = 128, zeros=None, tensor_scale: float = 1.0,
-                  swiglu: bool = False, accumulate: bool = False, stream=None):
+                  swiglu: bool = False, accumulate: bool = False, dev_status=None, stream=None):
     """out = x W^T (+ out) with the 4-bit weights codes [N, K/2] uint8 (element
     2i in the low nibble) and scales [N, ceil(K/group)]: fmt "int4" (scales
     fp32/bf16/fp16, zeros uint8 of the same shape or None for 8), "mxfp4" or
@@ -324,7 +324,7 @@ def moe_linear_w4(x, codes, scales, out, fmt="int4", group: int = 128, zeros=Non
     _done((_nat or _load_native()).linear_w4(
         x, codes, scales, out, zeros, LINEAR_FORMATS[fmt], group, tensor_scale,
         (MOE_LINEAR_SWIGLU if swiglu else 0) | (MOE_LINEAR_ACCUMULATE if accumulate else 0),
-        None if stream is None else _stream(stream)))
+        dev_status, None if stream is None else _stream(stream)))
 
 
 def moe_balance_loss_workspace_bytes(T: int, E: int, S: int = 1) -> int:

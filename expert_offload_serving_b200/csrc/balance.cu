@@ -90,19 +90,9 @@ __device__ __forceinline__ int offset_at(const int32_t* off, int i, int T) {
   return v < 0 ? 0 : (v > T ? T : v);
 }
 
-// The first sequence that ends after token t (S if none): the one that holds t, if any does.
-__device__ __forceinline__ int sequence_of(const int32_t* off, int S, int T, int t) {
-  int lo = 0, hi = S;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (offset_at(off, mid + 1, T) > t) hi = mid;
-    else lo = mid + 1;
-  }
-  return lo;
-}
-
-// The same for the token of a warp, 32 offsets at a time.
-__device__ __forceinline__ int sequence_of_warp(const int32_t* off, int S, int T, int t, int lane) {
+// The first sequence that ends after token t (S if none): the one that holds t, if
+// any does.  A whole warp looks, at 32 offsets at a time.
+__device__ __forceinline__ int sequence_of(const int32_t* off, int S, int T, int t, int lane) {
   int lo = 0, hi = S;                            // the answer lies in [lo, hi]
   while (lo < hi) {
     const int step = (hi - lo + 31) / 32;
@@ -252,7 +242,7 @@ __global__ void __launch_bounds__(kThreads) balance_partial_kernel(
   if (blockIdx.x == 0 && threadIdx.x == 0) *ws.ticket = 0;
   const int t0 = blockIdx.x * tile_tokens;
   const int t1 = min(T, t0 + tile_tokens);
-  for (int s = seq == nullptr ? 0 : sequence_of(seq, S, T, t0); s < S; ++s) {
+  for (int s = seq == nullptr ? 0 : sequence_of(seq, S, T, t0, lane); s < S; ++s) {
     const int a = seq == nullptr ? 0 : offset_at(seq, s, T), b = seq == nullptr ? T : offset_at(seq, s + 1, T);
     if (a >= t1) break;
     const int lo = max(a, t0), hi = min(b, t1);
@@ -502,7 +492,7 @@ __global__ void __launch_bounds__(kThreads) router_backward_kernel(
     float* row = dlogits + static_cast<size_t>(t) * E;
     bool live = counted >> (t - t0) & 1u;
     if (t >= seq_end) {                           // seq != nullptr
-      s = sequence_of_warp(seq, S, T, t, lane);
+      s = sequence_of(seq, S, T, t, lane);
       seq_begin = s < S ? offset_at(seq, s, T) : T;
       seq_end = s < S ? offset_at(seq, s + 1, T) : T;
       if (with_loss && s < S) cb0 = dl * __ldg(coef + s);

@@ -1,11 +1,15 @@
 // moe_linear_w4: argument checks and dispatch (the kernel: linear_w4.cuh).
+#include <cstdlib>
+#include <cstring>
+
 #include "linear_w4.cuh"
 
 using namespace moe;
 
 extern "C" moe_status moe_linear_w4(moe_linear_shape s, const void* codes, const void* scales, const uint8_t* zeros,
                                     float tensor_scale, const void* x, int x_type, int64_t ldx, int T, void* y,
-                                    int y_type, int64_t ldy, int flags, cudaStream_t stream) {
+                                    int y_type, int64_t ldy, int flags, int32_t* dev_status,
+                                    cudaStream_t stream) {
   clear_error();
   MOE_REQUIRE(s.N >= 1 && s.N <= (1 << 24), "N=%d outside [1, %d]", s.N, 1 << 24);
   MOE_REQUIRE(s.K >= 32 && s.K <= (1 << 17) && s.K % 32 == 0, "K=%d: a multiple of 32 up to %d", s.K, 1 << 17);
@@ -52,8 +56,12 @@ extern "C" moe_status moe_linear_w4(moe_linear_shape s, const void* codes, const
   P.accumulate = (flags & MOE_LINEAR_ACCUMULATE) != 0;
   P.tensor_scale = tensor_scale;
   const bool bf16 = x_type == MOE_DT_BF16;
-  const cudaError_t e = int4 ? launch_linear_int4(P, s.group, bf16, dev, stream)
-                             : launch_linear_fp4(P, s.fmt, bf16, dev, stream);
+  const char* force = getenv("MOE_LINEAR");
+  const bool tc = force != nullptr ? strcmp(force, "tc") == 0 : T > 16;
+  const cudaError_t e = tc ? (int4 ? launch_linear_tc_int4(P, s.group, bf16, dev, dev_status, stream)
+                                   : launch_linear_tc_fp4(P, s.fmt, bf16, dev, dev_status, stream))
+                           : (int4 ? launch_linear_int4(P, s.group, bf16, dev, stream)
+                                   : launch_linear_fp4(P, s.fmt, bf16, dev, stream));
   if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "linear_w4 launch: %s", cudaGetErrorString(e));
   return MOE_OK;
 }

@@ -53,6 +53,11 @@ struct LinearParams {
 // Launchers, one per format family (linear_w4_int4.cu, linear_w4_fp4.cu).
 cudaError_t launch_linear_int4(const LinearParams& P, int group, bool bf16, const DeviceInfo& dev, cudaStream_t s);
 cudaError_t launch_linear_fp4(const LinearParams& P, int fmt, bool bf16, const DeviceInfo& dev, cudaStream_t s);
+// The same on the 5th-generation tensor cores (linear_w4_tc_*.cu).
+cudaError_t launch_linear_tc_int4(const LinearParams& P, int group, bool bf16, const DeviceInfo& dev, int32_t* status,
+                                  cudaStream_t s);
+cudaError_t launch_linear_tc_fp4(const LinearParams& P, int fmt, bool bf16, const DeviceInfo& dev, int32_t* status,
+                                 cudaStream_t s);
 
 namespace w4 {
 

@@ -1,0 +1,483 @@
+// The dense 4-bit linear on the 5th-generation tensor cores.
+//
+// D[128 rows of W x NT tokens] += A[128 x 128 of K] x X^T a stage.  The codes
+// (8 KB) and the token rows of a stage arrive by TMA; eight warps turn the codes
+// into exact values of the x type (see linear_w4.cuh) in registers and write them
+// to tensor memory, where they are the A operand of tcgen05.mma kind::f16 -- no
+// trip of the expanded weights through shared memory, whose bandwidth two bytes a
+// weight would use up.  TMEM lane = row of W, so a thread works on one row
+// throughout: its zeros and scales are its own loads.
+//
+// Scales of INT4 and MXFP4 groups multiply the group's fp32 sum: the MMAs of a
+// group write an accumulator of their own, one of ND in turn, and the same eight
+// warps read it back and add it, scaled, to sums in registers while the tensor
+// core works on later groups.  (NVFP4's block scale goes into the weight, which
+// stays exact, and the accumulator runs through.)  So every product is exact here
+// too, and results differ from the other kernel's only by the order of fp32 sums.
+//
+// Warps 0-7: workers; quadrant (TMEM lanes) = warp % 4; warp / 4 = half of the
+// stage's K when expanding codes, half of the tokens when adding up.  Warp 8: TMA.
+// Warp 9: MMA.  Work is walked in the same order by all: output tiles dealt to
+// the CTAs, stages of K within.  Every wait is bounded: on expiry the CTA records
+// MOE_ERR_TIMEOUT, stops issuing, drains what it issued and frees its TMEM.
+#pragma once
+
+#include "linear_w4.cuh"
+#include "tc.cuh"
+
+namespace moe {
+namespace w4tc {
+
+using namespace ::moe::tc;
+
+constexpr int KS = 128;                       // K of a stage
+constexpr int TM = 128;                       // rows of W of a tile
+constexpr int kWorkers = 8;
+constexpr int kThreads = (kWorkers + 2) * 32;
+constexpr int kCodeBytes = TM * KS / 2;
+constexpr int kACols = KS / 2;                // TMEM columns of an A buffer (two 16-bit values a column)
+
+struct TcParams {
+  LinearParams L;
+  uint64_t wait_ns;
+  int stall, mt, tt;                          // tiles of rows, of tokens
+  int32_t* status;
+};
+
+template <int FMT, int GROUP, int NT>
+struct Cfg {
+  static constexpr bool POST = FMT != MOE_W_NVFP4;                     // the scale multiplies a group's sum
+  static constexpr int GPS = POST ? KS / GROUP : 1;                    // groups of a stage
+  static constexpr int CTAS = NT <= 32 ? 2 : 1;                        // CTAs on an SM
+  static constexpr int TMEM_COLS = NT <= 32 ? 256 : 512;
+  static constexpr int ND = (TMEM_COLS - 2 * kACols) / NT < 8 ? (TMEM_COLS - 2 * kACols) / NT : 8;
+  static constexpr int XB = NT * 128;                                  // 64 elements of the token rows
+  static constexpr int STAGE = kCodeBytes + 2 * XB;
+  static constexpr int S = (CTAS == 2 ? 108 * 1024 : 220 * 1024) / STAGE;
+  static constexpr int N_BARS = 2 * S + 4 + 2 * ND + 2;
+  static constexpr int BAR_BYTES = (N_BARS * 8 + 16 + 127) / 128 * 128;
+  static constexpr int SMEM = 1024 + S * STAGE + BAR_BYTES;
+  static_assert(SMEM <= (CTAS == 2 ? 113 * 1024 : 227 * 1024), "shared memory");
+  static_assert(STAGE % 1024 == 0 && S >= 3 && ND >= 2, "");
+};
+
+// Pair P (0..3) of a word in natural order: the codes 2P (low half) and 2P + 1.
+template <int FMT, bool BF16, int P>
+__device__ __forceinline__ uint32_t natural_pair(uint32_t w, uint32_t c) {
+  if constexpr (FMT == MOE_W_INT4 && BF16) {
+    // byte * 0x1001 has its low nibble at bit 0 and its high nibble at bit 16
+    const uint32_t b = P == 3 ? w >> 24 : __byte_perm(w, 0, 0x4440 | P);
+    return w4::sub2<true>(w4::and_or(b * 0x1001u, 0x000F000Fu, 0x43004300u), c);
+  } else if constexpr (FMT == MOE_W_INT4) {
+    // the byte in both halves: 1024 + low nibble, 1024 + 16 * high nibble; one
+    // fused multiply-add brings both to code - zero
+    const uint32_t b = __byte_perm(w, 0, 0x4040 | P | (P << 8));
+    uint32_t r;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;"
+        : "=r"(r)
+        : "r"(w4::and_or(b, 0x00F0000Fu, 0x64006400u)), "r"(0x2C003C00u), "r"(c));
+    return r;
+  } else {
+    uint32_t h;
+    asm("{ .reg .b8 b; cvt.u8.u32 b, %1; cvt.rn.f16x2.e2m1x2 %0, b; }" : "=r"(h) : "r"(w >> (8 * P)));
+    // bf16: exponent and mantissa 3 places down read as the value * 2^-112
+    if constexpr (BF16) return w4::mul2<true>(w4::and_or(h, 0x80008000u, (h >> 3) & 0x0FFF0FFFu), c);
+    return FMT == MOE_W_NVFP4 ? w4::mul2<false>(h, c) : h;
+  }
+}
+
+// The constant `c` of natural_pair from a zero point, or an E4M3 scale byte.
+template <int FMT, bool BF16>
+__device__ __forceinline__ uint32_t pair_constant(uint32_t raw) {
+  if constexpr (FMT == MOE_W_INT4)
+    return BF16 ? (0x4300u | raw) * 0x10001u : (0xE400u | raw) | ((0xD400u | raw << 4) << 16);
+  else if constexpr (FMT == MOE_W_MXFP4)
+    return 0x77807780u;                                                // 2^112 twice
+  const __half h = __half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(raw), __NV_E4M3));
+  const uint32_t u = BF16 ? __float_as_uint(__half2float(h) * 5.192296858534828e33f) >> 16 : __half_as_ushort(h);
+  return u | (u << 16);
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_load(uint32_t taddr, float (&v)[N]) {
+  if constexpr (N == 8) tmem_ld8(taddr, v);
+  else if constexpr (N == 16) tmem_ld16(taddr, v);
+  else if constexpr (N == 32) tmem_ld32(taddr, v);
+  else {
+#pragma unroll
+    for (int i = 0; i < N; i += 32) tmem_ld32(taddr + i, reinterpret_cast<float (&)[32]>(v[i]));
+  }
+}
+
+template <int FMT, int GROUP, bool BF16, int NT>
+__global__ void __launch_bounds__(kThreads, (Cfg<FMT, GROUP, NT>::CTAS))
+    linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
+                        const __grid_constant__ TcParams Q) {
+  using C = Cfg<FMT, GROUP, NT>;
+  const LinearParams& P = Q.L;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::S * C::STAGE);
+  uint64_t* full = bars;                      // [S] a stage's codes and token rows landed
+  uint64_t* empty = bars + C::S;              // [S] ... read by the workers and the MMAs
+  uint64_t* afull = bars + 2 * C::S;          // [2] expanded weights written
+  uint64_t* aempty = afull + 2;               // [2] ... and used
+  uint64_t* dfull = aempty + 2;               // [ND] an accumulator complete
+  uint64_t* dempty = dfull + C::ND;           // [ND] ... and read
+  uint64_t* drain = dempty + C::ND;
+  uint64_t* stall = drain + 1;                // never arrived on (testing aid)
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + C::N_BARS);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nst = (P.K + KS - 1) / KS, ntiles = Q.mt * Q.tt;
+  const int outs = P.swiglu ? P.N >> 1 : P.N, per = P.swiglu ? TM / 2 : TM;   // outputs: in all, of a tile
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::S; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], kWorkers + 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&afull[i], kWorkers);
+      mbar_init(&aempty[i], 1);
+    }
+    for (int i = 0; i < C::ND; ++i) {
+      mbar_init(&dfull[i], 1);
+      mbar_init(&dempty[i], kWorkers);
+    }
+    mbar_init(drain, 1);
+    mbar_init(stall, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kWorkers + 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_holder)),
+                 "r"(C::TMEM_COLS));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder, tmem_d = tmem + 2 * kACols;
+  pdl_wait();
+  pdl_trigger();
+
+  if (warp == kWorkers) {
+    // ------------------------------------------------------------ TMA
+    if (lane == 0) {
+      const uint64_t pol_w = Q.tt > 1 ? policy_evict_last() : policy_evict_first(), pol_x = policy_evict_last();
+      int slot = 0, issued = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int tile = blockIdx.x; tile < ntiles && ok; tile += gridDim.x) {
+        const int m = tile / Q.tt * per, t = tile % Q.tt * NT;
+        for (int s = 0; s < nst; ++s) {
+          if (!mbar_wait<true>(&empty[slot], phase ^ 1u, abort_flag, Q.wait_ns)) {
+            ok = false;
+            break;
+          }
+          uint8_t* at = smem + slot * C::STAGE;
+          mbar_expect_tx(&full[slot], C::STAGE);
+          tma_load_2d(at, &tm_w, &full[slot], s * (KS / 2), m, pol_w);
+          if (P.swiglu) tma_load_2d(at + kCodeBytes / 2, &tm_w, &full[slot], s * (KS / 2), outs + m, pol_w);
+#pragma unroll
+          for (int a = 0; a < 2; ++a)
+            tma_load_2d(at + kCodeBytes + a * C::XB, &tm_x, &full[slot], s * KS + a * 64, t, pol_x);
+          ++issued;
+          if (++slot == C::S) {
+            slot = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok) {
+        report(Q.status, MOE_ERR_TIMEOUT);
+        *abort_flag = 1;
+      }
+      for (int i = issued < C::S ? issued : C::S; i > 0; --i) {        // what was issued has landed
+        if (--slot < 0) {
+          slot = C::S - 1;
+          phase ^= 1u;
+        }
+        mbar_drain(&full[slot], phase);
+      }
+    }
+  } else if (warp == kWorkers + 1) {
+    // ------------------------------------------------------------ MMA
+    if (lane == 0) {
+      const uint32_t idesc = (1u << 4) | (BF16 ? (1u << 7) | (1u << 10) : 0u) |
+                             (static_cast<uint32_t>(NT >> 3) << 17) | (static_cast<uint32_t>(TM >> 4) << 24);
+      int slot = 0, d = 0, it = 0;
+      uint32_t phase = 0, dphase = 0;
+      bool ok = true;
+      for (int tile = blockIdx.x; tile < ntiles && ok; tile += gridDim.x) {
+        for (int s = 0; s < nst && ok; ++s, ++it) {
+          const int buf = it & 1;
+          if (!mbar_wait<true>(&full[slot], phase, abort_flag, Q.wait_ns) ||
+              !mbar_wait<true>(&afull[buf], (it >> 1) & 1, abort_flag, Q.wait_ns)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a_tmem = tmem + buf * kACols;
+          const uint8_t* xs = smem + slot * C::STAGE + kCodeBytes;
+          for (int j = 0; j < C::GPS; ++j) {
+            if (C::POST || s == 0) {
+              if (!mbar_wait<true>(&dempty[d], dphase ^ 1u, abort_flag, Q.wait_ns)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+            }
+            constexpr int MMAS = KS / 16 / C::GPS;
+#pragma unroll
+            for (int i = 0; i < MMAS; ++i) {
+              const int kk = j * MMAS + i;                             // K = 16: 8 columns of A, 32 bytes of x
+              const uint64_t db = desc_sw128(smem_u32(xs + (kk >> 2) * C::XB)) + 2 * (kk & 3);
+              tc_mma_f16_ts(tmem_d + d * NT, a_tmem + kk * 8, db, idesc, i > 0 || (!C::POST && s > 0) ? 1u : 0u);
+            }
+            if (C::POST || s == nst - 1) {
+              tc_commit(&dfull[d]);
+              if (++d == C::ND) {
+                d = 0;
+                dphase ^= 1u;
+              }
+            }
+          }
+          if (!ok) break;
+          tc_commit(&aempty[buf]);
+          tc_commit(&empty[slot]);
+          if (++slot == C::S) {
+            slot = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok) {
+        report(Q.status, MOE_ERR_TIMEOUT);
+        *abort_flag = 1;
+      }
+      tc_commit(drain);
+      mbar_drain(drain, 0);
+    }
+  } else {
+    // ------------------------------------------------------------ workers
+    const int quad = warp & 3, half = warp >> 2;
+    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+    // this thread's row: of the tile's outputs, and in the stage
+    const int out_row = P.swiglu ? quad * 16 + (lane & 15) : quad * 32 + lane;
+    const int srow = P.swiglu && lane >= 16 ? TM / 2 + out_row : out_row;
+    // codes of the half stage: two 16-byte chunks of the row, swizzled over 64 bytes
+    const uint32_t c0 = srow * 64 + (((2 * half) ^ ((srow >> 1) & 3)) << 4);
+    const uint32_t c1 = srow * 64 + (((2 * half + 1) ^ ((srow >> 1) & 3)) << 4);
+    constexpr int CN = NT / 2;                                         // tokens of this thread
+    constexpr int HC = FMT == MOE_W_NVFP4 ? 4 : FMT == MOE_W_INT4 && GROUP == 32 ? 2 : 1;   // constants of half a stage
+    constexpr int HK = 64 / HC;                                        // K of one
+    int slot = 0, d = 0, it = 0;
+    uint32_t phase = 0, dphase = 0;
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t ph) {
+      return __all_sync(kFull, mbar_wait<true>(bar, ph, abort_flag, Q.wait_ns)) != 0;
+    };
+    auto arrive = [&](uint64_t* bar) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
+    if (Q.stall && blockIdx.x == 0) ok = wait(stall, 0);               // testing aid: runs out
+    for (int tile = blockIdx.x; tile < ntiles && ok; tile += gridDim.x) {
+      const int first = tile / Q.tt * per, tok0 = tile % Q.tt * NT;
+      const int wrow = min(first + out_row, outs - 1) + (P.swiglu && lane >= 16 ? outs : 0);
+      const size_t sbase = static_cast<size_t>(wrow) * P.groups;
+      // raw constants of a stage's half (zeros, or block scales) and raw scales
+      auto fetch_c = [&](int s, uint32_t (&c)[HC]) {
+#pragma unroll
+        for (int i = 0; i < HC; ++i) {
+          const int k = s * KS + half * 64 + i * HK;
+          c[i] = FMT == MOE_W_INT4 ? 8u : 0u;
+          if (FMT == MOE_W_INT4 && P.zeros != nullptr && k < P.K) c[i] = __ldg(P.zeros + sbase + k / GROUP) & 15u;
+          if (FMT == MOE_W_NVFP4 && k < P.K) c[i] = __ldg(static_cast<const uint8_t*>(P.scales) + sbase + k / GROUP);
+        }
+      };
+      auto fetch_s = [&](int s, uint32_t (&f)[C::GPS]) {
+#pragma unroll
+        for (int j = 0; j < C::GPS; ++j) {
+          const int gi = s * C::GPS + j;
+          f[j] = 0;
+          if (!C::POST || gi >= P.groups) continue;
+          if (FMT == MOE_W_MXFP4) f[j] = 0x100u | __ldg(static_cast<const uint8_t*>(P.scales) + sbase + gi);
+          else if (P.scale_type == MOE_DT_F32) f[j] = __ldg(static_cast<const uint32_t*>(P.scales) + sbase + gi);
+          else f[j] = __ldg(static_cast<const uint16_t*>(P.scales) + sbase + gi);
+        }
+      };
+      auto scale_of = [&](uint32_t r) {
+        if (FMT == MOE_W_MXFP4) return r == 0 ? 0.f : w4::e8m0_value(r & 255u);
+        if (P.scale_type == MOE_DT_F32) return __uint_as_float(r);
+        if (P.scale_type == MOE_DT_BF16) return __uint_as_float(r << 16);
+        return __half2float(__ushort_as_half(static_cast<uint16_t>(r)));
+      };
+      float acc[CN];
+#pragma unroll
+      for (int i = 0; i < CN; ++i) acc[i] = 0.f;
+      uint32_t cn[HC], fn[C::GPS], fp[C::GPS];
+      fetch_c(0, cn);
+      fetch_s(0, fn);
+      // the accumulators of a stage, scaled, into acc
+      auto add_up = [&](const uint32_t (&f)[C::GPS]) {
+#pragma unroll
+        for (int j = 0; j < C::GPS; ++j) {
+          if (!wait(&dfull[d], dphase)) return false;
+          tc_fence_after();
+          float v[CN];
+          tmem_load(tmem_d + lanes + d * NT + half * CN, v);
+          tc_fence_before();
+          arrive(&dempty[d]);
+          if (++d == C::ND) {
+            d = 0;
+            dphase ^= 1u;
+          }
+          if constexpr (C::POST) {
+            const float sc = scale_of(f[j]);
+            const float2 s2 = make_float2(sc, sc);
+#pragma unroll
+            for (int i = 0; i < CN; i += 2) {
+              const float2 r = __ffma2_rn(make_float2(v[i], v[i + 1]), s2, make_float2(acc[i], acc[i + 1]));
+              acc[i] = r.x;
+              acc[i + 1] = r.y;
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < CN; ++i) acc[i] = v[i] * P.tensor_scale;
+          }
+        }
+        return true;
+      };
+      for (int s = 0; s < nst; ++s, ++it) {
+        const int buf = it & 1;
+        uint32_t c[HC];
+#pragma unroll
+        for (int i = 0; i < HC; ++i) c[i] = pair_constant<FMT, BF16>(cn[i]);
+        if (FMT == MOE_W_NVFP4) {
+#pragma unroll
+          for (int i = 0; i < HC; ++i)
+            if (s * KS + half * 64 + i * HK >= P.K) c[i] = 0;          // behind K
+        }
+        if (!wait(&full[slot], phase)) {
+          ok = false;
+          break;
+        }
+        const uint8_t* at = smem + slot * C::STAGE;
+        const uint4 q0 = *reinterpret_cast<const uint4*>(at + c0), q1 = *reinterpret_cast<const uint4*>(at + c1);
+        arrive(&empty[slot]);
+        if (++slot == C::S) {
+          slot = 0;
+          phase ^= 1u;
+        }
+        if (s + 1 < nst) fetch_c(s + 1, cn);
+        const uint32_t w[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+        uint32_t a[32];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t ci = c[i * 8 / HK];
+          a[4 * i] = natural_pair<FMT, BF16, 0>(w[i], ci);
+          a[4 * i + 1] = natural_pair<FMT, BF16, 1>(w[i], ci);
+          a[4 * i + 2] = natural_pair<FMT, BF16, 2>(w[i], ci);
+          a[4 * i + 3] = natural_pair<FMT, BF16, 3>(w[i], ci);
+        }
+        if (!wait(&aempty[buf], ((it >> 1) & 1) ^ 1u)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        tmem_st32(tmem + lanes + buf * kACols + half * 32, a);
+        tc_fence_before();
+        arrive(&afull[buf]);
+        if (C::POST) {
+          if (s > 0 && !add_up(fp)) {
+            ok = false;
+            break;
+          }
+#pragma unroll
+          for (int j = 0; j < C::GPS; ++j) fp[j] = fn[j];
+          if (s + 1 < nst) fetch_s(s + 1, fn);
+        }
+      }
+      if (!ok || !add_up(fp)) {
+        ok = false;
+        break;
+      }
+      // y[t][n]: lanes hold consecutive n
+      const int n = first + out_row;
+      if (P.swiglu) {
+        // lanes 0-15 hold h and 16-31 u of the same outputs: each half takes every other token
+#pragma unroll
+        for (int i = 0; i < CN; i += 2) {
+          const float got = __shfl_xor_sync(kFull, lane < 16 ? acc[i + 1] : acc[i], 16);
+          const float h = lane < 16 ? acc[i] : got, u = lane < 16 ? got : acc[i + 1];
+          const int t = tok0 + half * CN + i + (lane >> 4);
+          if (n < outs && t < P.T) w4::store_y<BF16>(P, t, n, h / (1.f + expf(-h)) * u);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < CN; ++i) {
+          const int t = tok0 + half * CN + i;
+          if (n < outs && t < P.T) w4::store_y<BF16>(P, t, n, acc[i]);
+        }
+      }
+    }
+    if (!ok) {
+      report(Q.status, MOE_ERR_TIMEOUT);
+      *abort_flag = 1;
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kWorkers + 1)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM_COLS));
+}
+
+template <int FMT, int GROUP, bool BF16, int NT>
+cudaError_t launch(const LinearParams& P, const DeviceInfo& dev, int32_t* status, cudaStream_t s) {
+  using C = Cfg<FMT, GROUP, NT>;
+  auto kern = linear_w4_tc_kernel<FMT, GROUP, BF16, NT>;
+  static bool done[64] = {};
+  if (!done[dev.id]) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    done[dev.id] = true;
+  }
+  TcParams Q{};
+  Q.L = P;
+  Q.wait_ns = wait_limit_ns();
+  Q.stall = test_stall();
+  Q.status = status;
+  const int outs = P.swiglu ? P.N / 2 : P.N, per = P.swiglu ? TM / 2 : TM;
+  Q.mt = (outs + per - 1) / per;
+  Q.tt = (P.T + NT - 1) / NT;
+  CUtensorMap tm_w, tm_x;
+  const uint64_t wd[2] = {static_cast<uint64_t>(P.K) / 2, static_cast<uint64_t>(P.N)}, ws[1] = {wd[0]};
+  const uint32_t wb[2] = {KS / 2, static_cast<uint32_t>(per)};
+  const uint64_t xd[2] = {static_cast<uint64_t>(P.K), static_cast<uint64_t>(P.T)},
+                 xs[1] = {static_cast<uint64_t>(P.ldx) * 2};
+  const uint32_t xb[2] = {64, NT};
+  if (encode_tiled_sw64(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, P.codes, wd, ws, wb) != CUDA_SUCCESS ||
+      encode_tiled_sw128(&tm_x, BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, P.x, xd,
+                         xs, xb) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  const int64_t tiles = static_cast<int64_t>(Q.mt) * Q.tt, most = static_cast<int64_t>(dev.sm_count) * C::CTAS;
+  const cudaError_t e = launch_pdl(kern, dim3(static_cast<unsigned>(tiles < most ? tiles : most)), dim3(kThreads),
+                                   C::SMEM, s, tm_w, tm_x, Q);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int FMT, int GROUP, bool BF16>
+cudaError_t launch_tokens(const LinearParams& P, const DeviceInfo& dev, int32_t* status, cudaStream_t s) {
+  if (P.T <= 16) return launch<FMT, GROUP, BF16, 16>(P, dev, status, s);
+  if (P.T <= 32) return launch<FMT, GROUP, BF16, 32>(P, dev, status, s);
+  if (P.T <= 64) return launch<FMT, GROUP, BF16, 64>(P, dev, status, s);
+  return launch<FMT, GROUP, BF16, 128>(P, dev, status, s);
+}
+
+}  // namespace w4tc
+}  // namespace moe

@@ -141,9 +141,9 @@ PyObject* guarded(const char* name, Py_ssize_t n, Py_ssize_t want, F f) {
   status = call;               \
   Py_END_ALLOW_THREADS
 
-// (x, codes, scales, out, zeros, fmt, group, tensor_scale, flags, stream)
+// (x, codes, scales, out, zeros, fmt, group, tensor_scale, flags, dev_status, stream)
 PyObject* linear_w4(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded("linear_w4", n, 10, [&] {
+  return guarded("linear_w4", n, 11, [&] {
     const at::Tensor &x = *tensor("x", a[0]), &codes = *tensor("codes", a[1]), &scales = *tensor("scales", a[2]),
                      &out = *tensor("out", a[3]);
     const at::Tensor* zeros = tensor("zeros", a[4], true);
@@ -169,10 +169,11 @@ PyObject* linear_w4(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const void* pz = matrix("zeros", zeros, N, G, at::kByte, dev);
     const int64_t ldx = row_distance("x", x, T, K, dev);
     const int64_t ldy = row_distance("out", out, T, flags & MOE_LINEAR_SWIGLU ? N / 2 : N, dev);
-    const cudaStream_t stream = stream_of(a[9], dev);
+    int32_t* status = static_cast<int32_t*>(mem("dev_status", tensor("dev_status", a[9], true), 1, at::kInt, dev));
+    const cudaStream_t stream = stream_of(a[10], dev);
     const int t = fits_int("T", T);
     MOE_CALL(r, moe_linear_w4(s, pc, ps, static_cast<const uint8_t*>(pz), static_cast<float>(ts), x.data_ptr(), xt, ldx,
-                              t, out.data_ptr(), yt, ldy, flags, stream))
+                              t, out.data_ptr(), yt, ldy, flags, status, stream))
     return r;
   });
 }

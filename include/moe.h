@@ -452,7 +452,9 @@ moe_status moe_profile_bandwidth(moe_shape s, const void* host_pool, int n_blobs
  *            Elements of y outside these rows are left as they were; y may not
  *            overlap x or the weights.
  * Products are exact, sums are fp32 in a fixed order (the same call gives the
- * same bits), y is rounded once.  x, scales, codes and y: codes and x 16-byte
+ * same bits), y is rounded once.  dev_status: device int32 word or NULL;
+ * MOE_ERR_TIMEOUT is recorded there if a bounded wait of the tcgen05 kernel runs
+ * out (y is then incomplete).  x, scales, codes and y: codes and x 16-byte
  * aligned, y and scales aligned to their element.  T >= 0 (T = 0 enqueues
  * nothing), T <= 1 << 20. */
 typedef enum moe_dtype { MOE_DT_F32 = 0, MOE_DT_BF16 = 1, MOE_DT_F16 = 2 } moe_dtype;
@@ -461,7 +463,7 @@ enum { MOE_LINEAR_SWIGLU = 1, MOE_LINEAR_ACCUMULATE = 2 };
 typedef struct moe_linear_shape { int32_t N, K, fmt, group, scale_type; } moe_linear_shape;
 moe_status moe_linear_w4(moe_linear_shape s, const void* codes, const void* scales, const uint8_t* zeros,
                          float tensor_scale, const void* x, int x_type, int64_t ldx, int T, void* y,
-                         int y_type, int64_t ldy, int flags, cudaStream_t stream);
+                         int y_type, int64_t ldy, int flags, int32_t* dev_status, cudaStream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* Balance loss and per-expert counts of a routing, and the router's gradient.

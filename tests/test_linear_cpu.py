@@ -35,7 +35,7 @@ def _call(moe, p, N=16, K=64, fmt=3, group=32, st=1, codes=0, scales=0, zeros=No
           ldy=16, flags=0):
     at = lambda v: None if v is None else p + v
     return moe.lib().moe_linear_w4(moe.moe_linear_shape(N, K, fmt, group, st), at(codes), at(scales), at(zeros), 1.0,
-                                   at(x), xt, ldx, T, at(y), yt, ldy, flags, None)
+                                   at(x), xt, ldx, T, at(y), yt, ldy, flags, None, None)
 
 
 @pytest.mark.parametrize("bad", [
@@ -55,7 +55,7 @@ def test_refusals(moe, bad):
 
 def test_no_tokens_is_no_call(moe):
     assert moe.lib().moe_linear_w4(moe.moe_linear_shape(16, 64, 3, 32, 1), None, None, None, 1.0, None, 1, 64, 0, None,
-                                   0, 16, 0, None) == moe.MOE_OK
+                                   0, 16, 0, None, None) == moe.MOE_OK
 
 
 @pytest.mark.skipif(torch.cuda.is_available(), reason="valid calls would launch on host pointers")
