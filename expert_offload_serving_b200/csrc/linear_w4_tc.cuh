@@ -8,18 +8,29 @@
 // weight would use up.  TMEM lane = row of W, so a thread works on one row
 // throughout: its zeros and scales are its own loads.
 //
-// Scales of INT4 and MXFP4 groups multiply the group's fp32 sum: the MMAs of a
-// group write an accumulator of their own, one of ND in turn, and the same eight
-// warps read it back and add it, scaled, to sums in registers while the tensor
-// core works on later groups.  (NVFP4's block scale goes into the weight, which
-// stays exact, and the accumulator runs through.)  So every product is exact here
-// too, and results differ from the other kernel's only by the order of fp32 sums.
+// Scales.  With bf16 x they go into the weights (PRE), and one fp32 accumulator
+// runs through all of K: an NVFP4 weight has 6 significant bits and an MXFP4 one
+// 2, exact in bf16; an INT4 weight (code - zero) * scale has up to 12 and becomes
+// the exact sum of two bf16 values, two A planes and two MMAs.  (A scale in fp16
+// or fp32 is itself taken as two bf16 values, and the weight is then within 2^-16.)
+// With f16 x, whose range does not hold every scale, INT4 and MXFP4 scales multiply
+// the group's fp32 sum (POST): the MMAs of a group write an accumulator of their
+// own, one of ND in turn, and the warps read it back and add it, scaled, to sums in
+// registers while the tensor core works on later groups.  The hand-overs that
+// takes cost more than the second plane: at T = 64, N = 16384, K = 4096 with groups
+// of 128, POST took 25 us in bf16.
 //
-// Warps 0-7: workers; quadrant (TMEM lanes) = warp % 4; warp / 4 = half of the
-// stage's K when expanding codes, half of the tokens when adding up.  Warp 8: TMA.
-// Warp 9: MMA.  Work is walked in the same order by all: output tiles dealt to
-// the CTAs, stages of K within.  Every wait is bounded: on expiry the CTA records
-// MOE_ERR_TIMEOUT, stops issuing, drains what it issued and frees its TMEM.
+// Two sets of eight warps take the stages in turn, each with its own A buffer,
+// accumulators and MMA-issuing warp: the hand-overs of a stage (codes landed ->
+// expanded -> multiplied -> added up) cost more time than its work, and the sets'
+// run side by side.  Warps 0-15: workers; quadrant (TMEM lanes) = warp % 4.
+// Expanding codes, warps 0-7 take the even stages and 8-15 the odd ones, four
+// warps a half of the stage's K.  Adding up, all take every stage, each a quarter
+// of the tokens.  Warp 16: TMA of the codes, 17: of the token rows.  Warps 18, 19:
+// MMAs of the even and the odd stages.  Work is walked in the same order by all:
+// output tiles dealt to the CTAs, stages of K within.  Every wait is bounded: on
+// expiry the CTA records MOE_ERR_TIMEOUT, stops issuing, drains what it issued and
+// frees its TMEM.
 #pragma once
 
 #include "linear_w4.cuh"
@@ -32,8 +43,8 @@ using namespace ::moe::tc;
 
 constexpr int KS = 128;                       // K of a stage
 constexpr int TM = 128;                       // rows of W of a tile
-constexpr int kWorkers = 8;
-constexpr int kThreads = (kWorkers + 2) * 32;
+constexpr int kWorkers = 16, kSet = 8;      // warps that expand a stage
+constexpr int kThreads = (kWorkers + 4) * 32;
 constexpr int kCodeBytes = TM * KS / 2;
 constexpr int kACols = KS / 2;                // TMEM columns of an A buffer (two 16-bit values a column)
 
@@ -44,21 +55,21 @@ struct TcParams {
   int32_t* status;
 };
 
-template <int FMT, int GROUP, int NT>
+template <int FMT, int GROUP, bool BF16, int NT>
 struct Cfg {
-  static constexpr bool POST = FMT != MOE_W_NVFP4;                     // the scale multiplies a group's sum
-  static constexpr int GPS = POST ? KS / GROUP : 1;                    // groups of a stage
-  static constexpr int CTAS = NT <= 32 ? 2 : 1;                        // CTAs on an SM
-  static constexpr int TMEM_COLS = NT <= 32 ? 256 : 512;
-  static constexpr int ND = (TMEM_COLS - 2 * kACols) / NT < 8 ? (TMEM_COLS - 2 * kACols) / NT : 8;
+  static constexpr bool POST = !BF16 && FMT != MOE_W_NVFP4;            // the scale multiplies a group's sum
+  static constexpr int PLANES = BF16 && FMT == MOE_W_INT4 ? 2 : 1;     // bf16 values of a weight
+  static constexpr int AC = PLANES * kACols;                           // TMEM columns of a set's A buffer
+  static constexpr int GPS = POST ? KS / GROUP : 1;                    // accumulators of a stage
+  static constexpr int ND = (512 - 2 * AC) / NT / 2 < 6 ? (512 - 2 * AC) / NT / 2 : 6;   // accumulators of a set
   static constexpr int XB = NT * 128;                                  // 64 elements of the token rows
   static constexpr int STAGE = kCodeBytes + 2 * XB;
-  static constexpr int S = (CTAS == 2 ? 108 * 1024 : 220 * 1024) / STAGE;
-  static constexpr int N_BARS = 2 * S + 4 + 2 * ND + 2;
+  static constexpr int S = 220 * 1024 / STAGE < 12 ? 220 * 1024 / STAGE : 12;
+  static constexpr int N_BARS = 2 * S + 4 + 4 * ND + 3;
   static constexpr int BAR_BYTES = (N_BARS * 8 + 16 + 127) / 128 * 128;
   static constexpr int SMEM = 1024 + S * STAGE + BAR_BYTES;
-  static_assert(SMEM <= (CTAS == 2 ? 113 * 1024 : 227 * 1024), "shared memory");
-  static_assert(STAGE % 1024 == 0 && S >= 3 && ND >= 2, "");
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+  static_assert(STAGE % 1024 == 0 && S >= 3 && ND >= 1, "");
 };
 
 // Pair P (0..3) of a word in natural order: the codes 2P (low half) and 2P + 1.
@@ -98,22 +109,48 @@ __device__ __forceinline__ uint32_t pair_constant(uint32_t raw) {
   return u | (u << 16);
 }
 
+// E8M0 as a bf16 pair, a quarter of it: 2^(b - 129), so that with 6 times it no
+// value leaves bf16's range (small ones are subnormals, which hold them exactly).
+// The sums are multiplied by 4.
+__device__ __forceinline__ uint32_t e8m0_quarter(uint32_t b) {
+  return (b == 255 ? 0x7FC0u : b < 3 ? 0x10u << b : (b - 2) << 7) * 0x10001u;
+}
+
+__device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
+  const __nv_bfloat162 r = __hfma2(reinterpret_cast<__nv_bfloat162&>(a), reinterpret_cast<__nv_bfloat162&>(b),
+                                   reinterpret_cast<__nv_bfloat162&>(c));
+  return reinterpret_cast<const uint32_t&>(r);
+}
+// a b - c
+__device__ __forceinline__ uint32_t fms2(uint32_t a, uint32_t b, uint32_t c) {
+  const __nv_bfloat162 r = __hfma2(reinterpret_cast<__nv_bfloat162&>(a), reinterpret_cast<__nv_bfloat162&>(b),
+                                   __hneg2(reinterpret_cast<__nv_bfloat162&>(c)));
+  return reinterpret_cast<const uint32_t&>(r);
+}
+
 template <int N>
 __device__ __forceinline__ void tmem_load(uint32_t taddr, float (&v)[N]) {
-  if constexpr (N == 8) tmem_ld8(taddr, v);
+  if constexpr (N == 4) tmem_ld4(taddr, v);
+  else if constexpr (N == 8) tmem_ld8(taddr, v);
   else if constexpr (N == 16) tmem_ld16(taddr, v);
-  else if constexpr (N == 32) tmem_ld32(taddr, v);
-  else {
-#pragma unroll
-    for (int i = 0; i < N; i += 32) tmem_ld32(taddr + i, reinterpret_cast<float (&)[32]>(v[i]));
-  }
+  else tmem_ld32(taddr, v);
+}
+
+// A bounded wait for hand-overs that are due within a stage.  The plain try_wait
+// suspends the thread in hardware for a while and wakes it at once; the form with
+// a time hint sleeps in coarse steps, which cost more than a stage each.  The
+// clock is read only after 64 looks in vain: reading it takes some 400 cycles.
+__device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint64_t limit_ns) {
+  for (int i = 0; i < 64; ++i)
+    if (mbar_try(bar, parity)) return true;
+  return mbar_wait<false>(bar, parity, abort_flag, limit_ns);
 }
 
 template <int FMT, int GROUP, bool BF16, int NT>
-__global__ void __launch_bounds__(kThreads, (Cfg<FMT, GROUP, NT>::CTAS))
+__global__ void __launch_bounds__(kThreads, 1)
     linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
                         const __grid_constant__ TcParams Q) {
-  using C = Cfg<FMT, GROUP, NT>;
+  using C = Cfg<FMT, GROUP, BF16, NT>;
   const LinearParams& P = Q.L;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -122,10 +159,10 @@ __global__ void __launch_bounds__(kThreads, (Cfg<FMT, GROUP, NT>::CTAS))
   uint64_t* empty = bars + C::S;              // [S] ... read by the workers and the MMAs
   uint64_t* afull = bars + 2 * C::S;          // [2] expanded weights written
   uint64_t* aempty = afull + 2;               // [2] ... and used
-  uint64_t* dfull = aempty + 2;               // [ND] an accumulator complete
-  uint64_t* dempty = dfull + C::ND;           // [ND] ... and read
-  uint64_t* drain = dempty + C::ND;
-  uint64_t* stall = drain + 1;                // never arrived on (testing aid)
+  uint64_t* dfull = aempty + 2;               // [2][ND] an accumulator complete
+  uint64_t* dempty = dfull + 2 * C::ND;       // [2][ND] ... and read
+  uint64_t* drain = dempty + 2 * C::ND;       // [2]
+  uint64_t* stall = drain + 2;                // never arrived on (testing aid)
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + C::N_BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -134,55 +171,61 @@ __global__ void __launch_bounds__(kThreads, (Cfg<FMT, GROUP, NT>::CTAS))
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::S; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], kWorkers + 1);
+      mbar_init(&full[s], 2);
+      mbar_init(&empty[s], kSet + 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&afull[i], kWorkers);
+      mbar_init(&afull[i], kSet);
       mbar_init(&aempty[i], 1);
     }
-    for (int i = 0; i < C::ND; ++i) {
+    for (int i = 0; i < 2 * C::ND; ++i) {
       mbar_init(&dfull[i], 1);
       mbar_init(&dempty[i], kWorkers);
     }
-    mbar_init(drain, 1);
+    mbar_init(&drain[0], 1);
+    mbar_init(&drain[1], 1);
     mbar_init(stall, 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == kWorkers + 1) {
+  if (warp == kWorkers + 2) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_holder)),
-                 "r"(C::TMEM_COLS));
+                 "n"(512));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_holder, tmem_d = tmem + 2 * kACols;
+  const uint32_t tmem = *tmem_holder, tmem_d = tmem + 2 * C::AC;
   pdl_wait();
   pdl_trigger();
 
-  if (warp == kWorkers) {
+  if (warp == kWorkers || warp == kWorkers + 1) {
     // ------------------------------------------------------------ TMA
+    const bool codes = warp == kWorkers;
     if (lane == 0) {
-      const uint64_t pol_w = Q.tt > 1 ? policy_evict_last() : policy_evict_first(), pol_x = policy_evict_last();
+      const uint64_t pol = codes && Q.tt == 1 ? policy_evict_first() : policy_evict_last();
       int slot = 0, issued = 0;
       uint32_t phase = 0;
       bool ok = true;
       for (int tile = blockIdx.x; tile < ntiles && ok; tile += gridDim.x) {
         const int m = tile / Q.tt * per, t = tile % Q.tt * NT;
         for (int s = 0; s < nst; ++s) {
-          if (!mbar_wait<true>(&empty[slot], phase ^ 1u, abort_flag, Q.wait_ns)) {
+          if (!wait_on(&empty[slot], phase ^ 1u, abort_flag, Q.wait_ns)) {
             ok = false;
             break;
           }
           uint8_t* at = smem + slot * C::STAGE;
-          mbar_expect_tx(&full[slot], C::STAGE);
-          tma_load_2d(at, &tm_w, &full[slot], s * (KS / 2), m, pol_w);
-          if (P.swiglu) tma_load_2d(at + kCodeBytes / 2, &tm_w, &full[slot], s * (KS / 2), outs + m, pol_w);
+          if (codes) {
+            mbar_expect_tx(&full[slot], kCodeBytes);
+            tma_load_2d(at, &tm_w, &full[slot], s * (KS / 2), m, pol);
+            if (P.swiglu) tma_load_2d(at + kCodeBytes / 2, &tm_w, &full[slot], s * (KS / 2), outs + m, pol);
+          } else {
+            mbar_expect_tx(&full[slot], 2 * C::XB);
 #pragma unroll
-          for (int a = 0; a < 2; ++a)
-            tma_load_2d(at + kCodeBytes + a * C::XB, &tm_x, &full[slot], s * KS + a * 64, t, pol_x);
+            for (int a = 0; a < 2; ++a)
+              tma_load_2d(at + kCodeBytes + a * C::XB, &tm_x, &full[slot], s * KS + a * 64, t, pol);
+          }
           ++issued;
           if (++slot == C::S) {
             slot = 0;
@@ -194,7 +237,10 @@ __global__ void __launch_bounds__(kThreads, (Cfg<FMT, GROUP, NT>::CTAS))
         report(Q.status, MOE_ERR_TIMEOUT);
         *abort_flag = 1;
       }
-      for (int i = issued < C::S ? issued : C::S; i > 0; --i) {        // what was issued has landed
+      // What was issued has landed before the CTA leaves.  (Where the other kind of
+      // a stage was never issued its barrier does not complete, and the bounded
+      // wait has long outlasted the copy.)
+      for (int i = issued < C::S ? issued : C::S; i > 0; --i) {
         if (--slot < 0) {
           slot = C::S - 1;
           phase ^= 1u;
@@ -202,67 +248,71 @@ __global__ void __launch_bounds__(kThreads, (Cfg<FMT, GROUP, NT>::CTAS))
         mbar_drain(&full[slot], phase);
       }
     }
-  } else if (warp == kWorkers + 1) {
+  } else if (warp >= kWorkers + 2) {
     // ------------------------------------------------------------ MMA
-    if (lane == 0) {
-      const uint32_t idesc = (1u << 4) | (BF16 ? (1u << 7) | (1u << 10) : 0u) |
-                             (static_cast<uint32_t>(NT >> 3) << 17) | (static_cast<uint32_t>(TM >> 4) << 24);
-      int slot = 0, d = 0, it = 0;
-      uint32_t phase = 0, dphase = 0;
-      bool ok = true;
-      for (int tile = blockIdx.x; tile < ntiles && ok; tile += gridDim.x) {
-        for (int s = 0; s < nst && ok; ++s, ++it) {
-          const int buf = it & 1;
-          if (!mbar_wait<true>(&full[slot], phase, abort_flag, Q.wait_ns) ||
-              !mbar_wait<true>(&afull[buf], (it >> 1) & 1, abort_flag, Q.wait_ns)) {
-            ok = false;
-            break;
+    const int set = warp - (kWorkers + 2);
+    const uint32_t idesc = (1u << 4) | (BF16 ? (1u << 7) | (1u << 10) : 0u) | (static_cast<uint32_t>(NT >> 3) << 17) |
+                           (static_cast<uint32_t>(TM >> 4) << 24);
+    const uint64_t xdesc = desc_sw128(smem_u32(smem + kCodeBytes));
+    const uint32_t a_tmem = tmem + set * C::AC, d_set = tmem_d + set * C::ND * NT;
+    uint64_t* const df = dfull + set * C::ND;
+    uint64_t* const de = dempty + set * C::ND;
+    int d = 0, base = 0;
+    uint32_t dphase = 0, aphase = 0;
+    bool ok = true;
+    // one verdict for the warp: its lanes take the same path
+    auto wait = [&](uint64_t* bar, uint32_t ph) {
+      return __all_sync(kFull, wait_on(bar, ph, abort_flag, Q.wait_ns)) != 0;
+    };
+    for (int tile = blockIdx.x; tile < ntiles && ok; tile += gridDim.x, base += nst) {
+      const int own0 = (base + set) & 1;
+      for (int s = own0; s < nst && ok; s += 2) {
+        const int g = base + s, slot = g % C::S;
+        ok = wait(&full[slot], (g / C::S) & 1) && wait(&afull[set], aphase);
+        if (!ok) break;
+        aphase ^= 1u;
+        const uint64_t xd = xdesc + (slot * C::STAGE >> 4);
+        const bool begin = C::POST || s == own0, end = C::POST || s + 2 >= nst;
+#pragma unroll
+        for (int j = 0; j < C::GPS; ++j) {
+          if (begin) {
+            ok = wait(&de[d], dphase ^ 1u);
+            if (!ok) break;
           }
           tc_fence_after();
-          const uint32_t a_tmem = tmem + buf * kACols;
-          const uint8_t* xs = smem + slot * C::STAGE + kCodeBytes;
-          for (int j = 0; j < C::GPS; ++j) {
-            if (C::POST || s == 0) {
-              if (!mbar_wait<true>(&dempty[d], dphase ^ 1u, abort_flag, Q.wait_ns)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-            }
-            constexpr int MMAS = KS / 16 / C::GPS;
+          constexpr int MMAS = KS / 16 / C::GPS;
+          if (elect_one()) {
 #pragma unroll
             for (int i = 0; i < MMAS; ++i) {
               const int kk = j * MMAS + i;                             // K = 16: 8 columns of A, 32 bytes of x
-              const uint64_t db = desc_sw128(smem_u32(xs + (kk >> 2) * C::XB)) + 2 * (kk & 3);
-              tc_mma_f16_ts(tmem_d + d * NT, a_tmem + kk * 8, db, idesc, i > 0 || (!C::POST && s > 0) ? 1u : 0u);
+              const uint64_t db = xd + (((kk >> 2) * C::XB) >> 4) + 2 * (kk & 3);
+              tc_mma_f16_ts(d_set + d * NT, a_tmem + kk * 8, db, idesc, i > 0 || !begin ? 1u : 0u);
+              if (C::PLANES == 2) tc_mma_f16_ts(d_set + d * NT, a_tmem + kACols + kk * 8, db, idesc, 1u);
             }
-            if (C::POST || s == nst - 1) {
-              tc_commit(&dfull[d]);
-              if (++d == C::ND) {
-                d = 0;
-                dphase ^= 1u;
-              }
+            if (end) tc_commit(&df[d]);
+            if (j == C::GPS - 1) {
+              tc_commit(&aempty[set]);
+              tc_commit(&empty[slot]);
             }
           }
-          if (!ok) break;
-          tc_commit(&aempty[buf]);
-          tc_commit(&empty[slot]);
-          if (++slot == C::S) {
-            slot = 0;
-            phase ^= 1u;
+          __syncwarp();
+          if (end && ++d == C::ND) {
+            d = 0;
+            dphase ^= 1u;
           }
         }
       }
-      if (!ok) {
-        report(Q.status, MOE_ERR_TIMEOUT);
-        *abort_flag = 1;
-      }
-      tc_commit(drain);
-      mbar_drain(drain, 0);
     }
+    if (!ok) {
+      report(Q.status, MOE_ERR_TIMEOUT);
+      *abort_flag = 1;
+    }
+    if (elect_one()) tc_commit(&drain[set]);
+    __syncwarp();
+    mbar_drain(&drain[set], 0);
   } else {
     // ------------------------------------------------------------ workers
-    const int quad = warp & 3, half = warp >> 2;
+    const int quad = warp & 3, set = warp >> 3, half = (warp >> 2) & 1, quarter = warp >> 2;
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
     // this thread's row: of the tile's outputs, and in the stage
     const int out_row = P.swiglu ? quad * 16 + (lane & 15) : quad * 32 + lane;
@@ -270,41 +320,47 @@ __global__ void __launch_bounds__(kThreads, (Cfg<FMT, GROUP, NT>::CTAS))
     // codes of the half stage: two 16-byte chunks of the row, swizzled over 64 bytes
     const uint32_t c0 = srow * 64 + (((2 * half) ^ ((srow >> 1) & 3)) << 4);
     const uint32_t c1 = srow * 64 + (((2 * half + 1) ^ ((srow >> 1) & 3)) << 4);
-    constexpr int CN = NT / 2;                                         // tokens of this thread
-    constexpr int HC = FMT == MOE_W_NVFP4 ? 4 : FMT == MOE_W_INT4 && GROUP == 32 ? 2 : 1;   // constants of half a stage
+    constexpr int CN = NT / 4;                                         // tokens of this thread
+    constexpr int HC = FMT == MOE_W_NVFP4 ? 4 : GROUP == 32 ? 2 : 1;   // groups of half a stage
     constexpr int HK = 64 / HC;                                        // K of one
-    int slot = 0, d = 0, it = 0;
-    uint32_t phase = 0, dphase = 0;
+    int base = 0, d[2] = {0, 0};                                       // base: stages of the tiles before this one
+    uint32_t dphase[2] = {0, 0}, aphase = 0;
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t ph) {
-      return __all_sync(kFull, mbar_wait<true>(bar, ph, abort_flag, Q.wait_ns)) != 0;
+      return __all_sync(kFull, wait_on(bar, ph, abort_flag, Q.wait_ns)) != 0;
     };
     auto arrive = [&](uint64_t* bar) {
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     };
     if (Q.stall && blockIdx.x == 0) ok = wait(stall, 0);               // testing aid: runs out
-    for (int tile = blockIdx.x; tile < ntiles && ok; tile += gridDim.x) {
+    for (int tile = blockIdx.x; tile < ntiles && ok; tile += gridDim.x, base += nst) {
       const int first = tile / Q.tt * per, tok0 = tile % Q.tt * NT;
       const int wrow = min(first + out_row, outs - 1) + (P.swiglu && lane >= 16 ? outs : 0);
       const size_t sbase = static_cast<size_t>(wrow) * P.groups;
-      // raw constants of a stage's half (zeros, or block scales) and raw scales
-      auto fetch_c = [&](int s, uint32_t (&c)[HC]) {
+      // raw zeros and scales of a stage's half (0x10000 or more: there is one) ...
+      auto fetch_c = [&](int s, uint32_t (&z)[HC], uint32_t (&f)[HC]) {
 #pragma unroll
         for (int i = 0; i < HC; ++i) {
           const int k = s * KS + half * 64 + i * HK;
-          c[i] = FMT == MOE_W_INT4 ? 8u : 0u;
-          if (FMT == MOE_W_INT4 && P.zeros != nullptr && k < P.K) c[i] = __ldg(P.zeros + sbase + k / GROUP) & 15u;
-          if (FMT == MOE_W_NVFP4 && k < P.K) c[i] = __ldg(static_cast<const uint8_t*>(P.scales) + sbase + k / GROUP);
+          z[i] = 8u;
+          f[i] = 0;
+          if (k >= P.K) continue;
+          const size_t at = sbase + k / GROUP;
+          if (FMT == MOE_W_INT4 && P.zeros != nullptr) z[i] = __ldg(P.zeros + at) & 15u;
+          if (FMT != MOE_W_INT4) f[i] = 0x10000u | __ldg(static_cast<const uint8_t*>(P.scales) + at);
+          else if (!C::POST && P.scale_type == MOE_DT_F32) f[i] = __ldg(static_cast<const uint32_t*>(P.scales) + at);
+          else if (!C::POST) f[i] = __ldg(static_cast<const uint16_t*>(P.scales) + at);
         }
       };
+      // ... and the scales of a whole stage's groups (POST)
       auto fetch_s = [&](int s, uint32_t (&f)[C::GPS]) {
 #pragma unroll
         for (int j = 0; j < C::GPS; ++j) {
           const int gi = s * C::GPS + j;
           f[j] = 0;
           if (!C::POST || gi >= P.groups) continue;
-          if (FMT == MOE_W_MXFP4) f[j] = 0x100u | __ldg(static_cast<const uint8_t*>(P.scales) + sbase + gi);
+          if (FMT == MOE_W_MXFP4) f[j] = 0x10000u | __ldg(static_cast<const uint8_t*>(P.scales) + sbase + gi);
           else if (P.scale_type == MOE_DT_F32) f[j] = __ldg(static_cast<const uint32_t*>(P.scales) + sbase + gi);
           else f[j] = __ldg(static_cast<const uint16_t*>(P.scales) + sbase + gi);
         }
@@ -318,93 +374,119 @@ __global__ void __launch_bounds__(kThreads, (Cfg<FMT, GROUP, NT>::CTAS))
       float acc[CN];
 #pragma unroll
       for (int i = 0; i < CN; ++i) acc[i] = 0.f;
-      uint32_t cn[HC], fn[C::GPS], fp[C::GPS];
-      fetch_c(0, cn);
+      const int own0 = (base + set) & 1;                               // this set's first stage of the tile
+      uint32_t zn[HC], sn[HC], fn[C::GPS];
+      fetch_c(own0, zn, sn);
       fetch_s(0, fn);
-      // the accumulators of a stage, scaled, into acc
-      auto add_up = [&](const uint32_t (&f)[C::GPS]) {
+      // An accumulator of a set, times sc, into acc.
+      auto take = [&](int st, float sc) {
+        uint64_t* const df = dfull + st * C::ND;
+        if (!wait(&df[d[st]], dphase[st])) return false;
+        tc_fence_after();
+        float v[CN];
+        tmem_load(tmem_d + lanes + (st * C::ND + d[st]) * NT + quarter * CN, v);
+        tc_fence_before();
+        arrive(&dempty[st * C::ND + d[st]]);
+        if (++d[st] == C::ND) {
+          d[st] = 0;
+          dphase[st] ^= 1u;
+        }
+        const float2 s2 = make_float2(sc, sc);
 #pragma unroll
-        for (int j = 0; j < C::GPS; ++j) {
-          if (!wait(&dfull[d], dphase)) return false;
-          tc_fence_after();
-          float v[CN];
-          tmem_load(tmem_d + lanes + d * NT + half * CN, v);
-          tc_fence_before();
-          arrive(&dempty[d]);
-          if (++d == C::ND) {
-            d = 0;
-            dphase ^= 1u;
-          }
-          if constexpr (C::POST) {
-            const float sc = scale_of(f[j]);
-            const float2 s2 = make_float2(sc, sc);
-#pragma unroll
-            for (int i = 0; i < CN; i += 2) {
-              const float2 r = __ffma2_rn(make_float2(v[i], v[i + 1]), s2, make_float2(acc[i], acc[i + 1]));
-              acc[i] = r.x;
-              acc[i + 1] = r.y;
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < CN; ++i) acc[i] = v[i] * P.tensor_scale;
-          }
+        for (int i = 0; i < CN; i += 2) {
+          const float2 r = __ffma2_rn(make_float2(v[i], v[i + 1]), s2, make_float2(acc[i], acc[i + 1]));
+          acc[i] = r.x;
+          acc[i + 1] = r.y;
         }
         return true;
       };
-      for (int s = 0; s < nst; ++s, ++it) {
-        const int buf = it & 1;
-        uint32_t c[HC];
+      // The groups of stage s; the next stage's scales are on their way meanwhile.
+      auto add_up = [&](int s) {
+        float f[C::GPS];
 #pragma unroll
-        for (int i = 0; i < HC; ++i) c[i] = pair_constant<FMT, BF16>(cn[i]);
-        if (FMT == MOE_W_NVFP4) {
+        for (int j = 0; j < C::GPS; ++j) f[j] = scale_of(fn[j]);
+        if (s + 1 < nst) fetch_s(s + 1, fn);
+        const bool odd = (base + s) & 1;
 #pragma unroll
-          for (int i = 0; i < HC; ++i)
-            if (s * KS + half * 64 + i * HK >= P.K) c[i] = 0;          // behind K
+        for (int j = 0; j < C::GPS; ++j)
+          if (!(odd ? take(1, f[j]) : take(0, f[j]))) return false;
+        return true;
+      };
+      int next = 0;                                                    // the next stage to add up
+      for (int s = own0; s < nst && ok; s += 2) {
+        // Stages up to s - 2 are added up before the wait for the buffer that stage
+        // s - 2's MMAs read: these may in turn wait for accumulators (a stage can
+        // have more groups than there are accumulators).
+        for (; C::POST && next < s - 1 && ok; ++next) ok = add_up(next);
+        const int g = base + s, slot = g % C::S;                       // stage g of all
+        uint32_t c[HC], s1[HC], s2[HC];
+#pragma unroll
+        for (int i = 0; i < HC; ++i) {
+          s1[i] = s2[i] = 0;
+          if (FMT == MOE_W_NVFP4) {
+            c[i] = sn[i] == 0 ? 0u : pair_constant<FMT, BF16>(sn[i] & 255u);
+          } else {
+            c[i] = pair_constant<FMT, BF16>(zn[i]);
+            if (!C::POST && FMT == MOE_W_MXFP4) s1[i] = sn[i] == 0 ? 0u : e8m0_quarter(sn[i] & 255u);
+            if (!C::POST && FMT == MOE_W_INT4) {
+              const float f = scale_of(sn[i]);
+              const __nv_bfloat16 hi = __float2bfloat16_rn(f);
+              s1[i] = __bfloat16_as_ushort(hi) * 0x10001u;
+              s2[i] = __bfloat16_as_ushort(__float2bfloat16_rn(f - __bfloat162float(hi))) * 0x10001u;
+            }
+          }
         }
-        if (!wait(&full[slot], phase)) {
+        if (!ok || !wait(&full[slot], (g / C::S) & 1)) {
           ok = false;
           break;
         }
         const uint8_t* at = smem + slot * C::STAGE;
         const uint4 q0 = *reinterpret_cast<const uint4*>(at + c0), q1 = *reinterpret_cast<const uint4*>(at + c1);
         arrive(&empty[slot]);
-        if (++slot == C::S) {
-          slot = 0;
-          phase ^= 1u;
-        }
-        if (s + 1 < nst) fetch_c(s + 1, cn);
+        if (s + 2 < nst) fetch_c(s + 2, zn, sn);
         const uint32_t w[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
-        uint32_t a[32];
+        uint32_t a[32], lo[C::PLANES == 2 ? 32 : 1];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const uint32_t ci = c[i * 8 / HK];
-          a[4 * i] = natural_pair<FMT, BF16, 0>(w[i], ci);
-          a[4 * i + 1] = natural_pair<FMT, BF16, 1>(w[i], ci);
-          a[4 * i + 2] = natural_pair<FMT, BF16, 2>(w[i], ci);
-          a[4 * i + 3] = natural_pair<FMT, BF16, 3>(w[i], ci);
+          const int h = i * 8 / HK;
+          a[4 * i] = natural_pair<FMT, BF16, 0>(w[i], c[h]);
+          a[4 * i + 1] = natural_pair<FMT, BF16, 1>(w[i], c[h]);
+          a[4 * i + 2] = natural_pair<FMT, BF16, 2>(w[i], c[h]);
+          a[4 * i + 3] = natural_pair<FMT, BF16, 3>(w[i], c[h]);
+          if constexpr (!C::POST && FMT == MOE_W_MXFP4) {
+#pragma unroll
+            for (int p = 4 * i; p < 4 * i + 4; ++p) a[p] = w4::mul2<true>(a[p], s1[h]);
+          }
+          if constexpr (C::PLANES == 2) {
+            // (code - zero) * scale = hi + lo: hi rounded, lo what is left, exact
+#pragma unroll
+            for (int p = 4 * i; p < 4 * i + 4; ++p) {
+              const uint32_t v = a[p];
+              a[p] = w4::mul2<true>(v, s1[h]);
+              lo[p] = fms2(v, s1[h], a[p]);
+              if (P.scale_type != MOE_DT_BF16) lo[p] = fma2(v, s2[h], lo[p]);
+            }
+          }
         }
-        if (!wait(&aempty[buf], ((it >> 1) & 1) ^ 1u)) {
+        if (!wait(&aempty[set], aphase ^ 1u)) {
           ok = false;
           break;
         }
+        aphase ^= 1u;
         tc_fence_after();
-        tmem_st32(tmem + lanes + buf * kACols + half * 32, a);
+        tmem_st32(tmem + lanes + set * C::AC + half * 32, a);
+        if constexpr (C::PLANES == 2) tmem_st32(tmem + lanes + set * C::AC + kACols + half * 32, lo);
         tc_fence_before();
-        arrive(&afull[buf]);
-        if (C::POST) {
-          if (s > 0 && !add_up(fp)) {
-            ok = false;
-            break;
-          }
-#pragma unroll
-          for (int j = 0; j < C::GPS; ++j) fp[j] = fn[j];
-          if (s + 1 < nst) fetch_s(s + 1, fn);
-        }
+        arrive(&afull[set]);
       }
-      if (!ok || !add_up(fp)) {
-        ok = false;
-        break;
+      if (C::POST) {
+        for (; next < nst && ok; ++next) ok = add_up(next);
+      } else {                                                         // one accumulator a set, over its stages
+        const float sc = FMT == MOE_W_NVFP4 ? P.tensor_scale : FMT == MOE_W_MXFP4 ? 4.f : 1.f;
+        if (ok && (nst > 1 || (base & 1) == 0)) ok = take(0, sc);
+        if (ok && (nst > 1 || (base & 1) == 1)) ok = take(1, sc);
       }
+      if (!ok) break;
       // y[t][n]: lanes hold consecutive n
       const int n = first + out_row;
       if (P.swiglu) {
@@ -413,13 +495,13 @@ __global__ void __launch_bounds__(kThreads, (Cfg<FMT, GROUP, NT>::CTAS))
         for (int i = 0; i < CN; i += 2) {
           const float got = __shfl_xor_sync(kFull, lane < 16 ? acc[i + 1] : acc[i], 16);
           const float h = lane < 16 ? acc[i] : got, u = lane < 16 ? got : acc[i + 1];
-          const int t = tok0 + half * CN + i + (lane >> 4);
+          const int t = tok0 + quarter * CN + i + (lane >> 4);
           if (n < outs && t < P.T) w4::store_y<BF16>(P, t, n, h / (1.f + expf(-h)) * u);
         }
       } else {
 #pragma unroll
         for (int i = 0; i < CN; ++i) {
-          const int t = tok0 + half * CN + i;
+          const int t = tok0 + quarter * CN + i;
           if (n < outs && t < P.T) w4::store_y<BF16>(P, t, n, acc[i]);
         }
       }
@@ -433,13 +515,13 @@ __global__ void __launch_bounds__(kThreads, (Cfg<FMT, GROUP, NT>::CTAS))
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kWorkers + 1)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM_COLS));
+  if (warp == kWorkers + 2)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512));
 }
 
 template <int FMT, int GROUP, bool BF16, int NT>
 cudaError_t launch(const LinearParams& P, const DeviceInfo& dev, int32_t* status, cudaStream_t s) {
-  using C = Cfg<FMT, GROUP, NT>;
+  using C = Cfg<FMT, GROUP, BF16, NT>;
   auto kern = linear_w4_tc_kernel<FMT, GROUP, BF16, NT>;
   static bool done[64] = {};
   if (!done[dev.id]) {
@@ -465,7 +547,7 @@ cudaError_t launch(const LinearParams& P, const DeviceInfo& dev, int32_t* status
       encode_tiled_sw128(&tm_x, BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, P.x, xd,
                          xs, xb) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
-  const int64_t tiles = static_cast<int64_t>(Q.mt) * Q.tt, most = static_cast<int64_t>(dev.sm_count) * C::CTAS;
+  const int64_t tiles = static_cast<int64_t>(Q.mt) * Q.tt, most = dev.sm_count;
   const cudaError_t e = launch_pdl(kern, dim3(static_cast<unsigned>(tiles < most ? tiles : most)), dim3(kThreads),
                                    C::SMEM, s, tm_w, tm_x, Q);
   return e != cudaSuccess ? e : cudaGetLastError();
