@@ -33,6 +33,8 @@
 // frees its TMEM.
 #pragma once
 
+#include <type_traits>
+
 #include "linear_w4.cuh"
 #include "tc.cuh"
 
@@ -46,6 +48,7 @@ constexpr int TM = 128;                       // rows of W of a tile
 constexpr int kWorkers = 16, kSet = 8;      // warps that expand a stage
 constexpr int kThreads = (kWorkers + 4) * 32;
 constexpr int kCodeBytes = TM * KS / 2;
+constexpr uint32_t kNegateA = 1u << 13;       // instruction descriptor: A counts negated
 constexpr int kACols = KS / 2;                // TMEM columns of an A buffer (two 16-bit values a column)
 
 struct TcParams {
@@ -73,21 +76,14 @@ struct Cfg {
 };
 
 // Pair P (0..3) of a word in natural order: the codes 2P (low half) and 2P + 1.
+// `up` is the word shifted right by a nibble.
 template <int FMT, bool BF16, int P>
-__device__ __forceinline__ uint32_t natural_pair(uint32_t w, uint32_t c) {
-  if constexpr (FMT == MOE_W_INT4 && BF16) {
-    // byte * 0x1001 has its low nibble at bit 0 and its high nibble at bit 16
-    const uint32_t b = P == 3 ? w >> 24 : __byte_perm(w, 0, 0x4440 | P);
-    return w4::sub2<true>(w4::and_or(b * 0x1001u, 0x000F000Fu, 0x43004300u), c);
-  } else if constexpr (FMT == MOE_W_INT4) {
-    // the byte in both halves: 1024 + low nibble, 1024 + 16 * high nibble; one
-    // fused multiply-add brings both to code - zero
-    const uint32_t b = __byte_perm(w, 0, 0x4040 | P | (P << 8));
-    uint32_t r;
-    asm("fma.rn.f16x2 %0, %1, %2, %3;"
-        : "=r"(r)
-        : "r"(w4::and_or(b, 0x00F0000Fu, 0x64006400u)), "r"(0x2C003C00u), "r"(c));
-    return r;
+__device__ __forceinline__ uint32_t natural_pair(uint32_t w, uint32_t up, uint32_t c) {
+  if constexpr (FMT == MOE_W_INT4) {
+    // byte P of the word to the low half, of the shifted word to the high half
+    // (the other two bytes are masked away)
+    const uint32_t b = __byte_perm(w, up, P | (P << 4) | ((4 + P) << 8) | ((4 + P) << 12));
+    return w4::sub2<BF16>(w4::and_or(b, 0x000F000Fu, BF16 ? 0x43004300u : 0x64006400u), c);
   } else {
     uint32_t h;
     asm("{ .reg .b8 b; cvt.u8.u32 b, %1; cvt.rn.f16x2.e2m1x2 %0, b; }" : "=r"(h) : "r"(w >> (8 * P)));
@@ -101,7 +97,7 @@ __device__ __forceinline__ uint32_t natural_pair(uint32_t w, uint32_t c) {
 template <int FMT, bool BF16>
 __device__ __forceinline__ uint32_t pair_constant(uint32_t raw) {
   if constexpr (FMT == MOE_W_INT4)
-    return BF16 ? (0x4300u | raw) * 0x10001u : (0xE400u | raw) | ((0xD400u | raw << 4) << 16);
+    return ((BF16 ? 0x4300u : 0x6400u) | raw) * 0x10001u;
   else if constexpr (FMT == MOE_W_MXFP4)
     return 0x77807780u;                                                // 2^112 twice
   const __half h = __half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(raw), __NV_E4M3));
@@ -121,13 +117,6 @@ __device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
                                    reinterpret_cast<__nv_bfloat162&>(c));
   return reinterpret_cast<const uint32_t&>(r);
 }
-// a b - c
-__device__ __forceinline__ uint32_t fms2(uint32_t a, uint32_t b, uint32_t c) {
-  const __nv_bfloat162 r = __hfma2(reinterpret_cast<__nv_bfloat162&>(a), reinterpret_cast<__nv_bfloat162&>(b),
-                                   __hneg2(reinterpret_cast<__nv_bfloat162&>(c)));
-  return reinterpret_cast<const uint32_t&>(r);
-}
-
 template <int N>
 __device__ __forceinline__ void tmem_load(uint32_t taddr, float (&v)[N]) {
   if constexpr (N == 4) tmem_ld4(taddr, v);
@@ -257,8 +246,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t a_tmem = tmem + set * C::AC, d_set = tmem_d + set * C::ND * NT;
     uint64_t* const df = dfull + set * C::ND;
     uint64_t* const de = dempty + set * C::ND;
-    int d = 0, base = 0;
-    uint32_t dphase = 0, aphase = 0;
+    int d = 0, base = 0, slot = set;                                   // slot: of this set's next stage
+    uint32_t dphase = 0, aphase = 0, phase = 0;
     bool ok = true;
     // one verdict for the warp: its lanes take the same path
     auto wait = [&](uint64_t* bar, uint32_t ph) {
@@ -267,8 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int tile = blockIdx.x; tile < ntiles && ok; tile += gridDim.x, base += nst) {
       const int own0 = (base + set) & 1;
       for (int s = own0; s < nst && ok; s += 2) {
-        const int g = base + s, slot = g % C::S;
-        ok = wait(&full[slot], (g / C::S) & 1) && wait(&afull[set], aphase);
+        ok = wait(&full[slot], phase) && wait(&afull[set], aphase);
         if (!ok) break;
         aphase ^= 1u;
         const uint64_t xd = xdesc + (slot * C::STAGE >> 4);
@@ -286,7 +274,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < MMAS; ++i) {
               const int kk = j * MMAS + i;                             // K = 16: 8 columns of A, 32 bytes of x
               const uint64_t db = xd + (((kk >> 2) * C::XB) >> 4) + 2 * (kk & 3);
-              tc_mma_f16_ts(d_set + d * NT, a_tmem + kk * 8, db, idesc, i > 0 || !begin ? 1u : 0u);
+              tc_mma_f16_ts(d_set + d * NT, a_tmem + kk * 8, db, C::PLANES == 2 ? idesc | kNegateA : idesc,
+                            i > 0 || !begin ? 1u : 0u);
               if (C::PLANES == 2) tc_mma_f16_ts(d_set + d * NT, a_tmem + kACols + kk * 8, db, idesc, 1u);
             }
             if (end) tc_commit(&df[d]);
@@ -300,6 +289,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             d = 0;
             dphase ^= 1u;
           }
+        }
+        if ((slot += 2) >= C::S) {
+          slot -= C::S;
+          phase ^= 1u;
         }
       }
     }
@@ -323,8 +316,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int CN = NT / 4;                                         // tokens of this thread
     constexpr int HC = FMT == MOE_W_NVFP4 ? 4 : GROUP == 32 ? 2 : 1;   // groups of half a stage
     constexpr int HK = 64 / HC;                                        // K of one
-    int base = 0, d[2] = {0, 0};                                       // base: stages of the tiles before this one
-    uint32_t dphase[2] = {0, 0}, aphase = 0;
+    int base = 0, d[2] = {0, 0}, slot = set;                           // base: stages of the tiles before this one
+    uint32_t dphase[2] = {0, 0}, aphase = 0, phase = 0;                // slot: of this set's next stage
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t ph) {
       return __all_sync(kFull, wait_on(bar, ph, abort_flag, Q.wait_ns)) != 0;
@@ -418,7 +411,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         // s - 2's MMAs read: these may in turn wait for accumulators (a stage can
         // have more groups than there are accumulators).
         for (; C::POST && next < s - 1 && ok; ++next) ok = add_up(next);
-        const int g = base + s, slot = g % C::S;                       // stage g of all
         uint32_t c[HC], s1[HC], s2[HC];
 #pragma unroll
         for (int i = 0; i < HC; ++i) {
@@ -436,38 +428,49 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if (!ok || !wait(&full[slot], (g / C::S) & 1)) {
+        if (!ok || !wait(&full[slot], phase)) {
           ok = false;
           break;
         }
         const uint8_t* at = smem + slot * C::STAGE;
         const uint4 q0 = *reinterpret_cast<const uint4*>(at + c0), q1 = *reinterpret_cast<const uint4*>(at + c1);
         arrive(&empty[slot]);
+        if ((slot += 2) >= C::S) {
+          slot -= C::S;
+          phase ^= 1u;
+        }
         if (s + 2 < nst) fetch_c(s + 2, zn, sn);
         const uint32_t w[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
         uint32_t a[32], lo[C::PLANES == 2 ? 32 : 1];
+        auto expand = [&](auto third) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int h = i * 8 / HK;
-          a[4 * i] = natural_pair<FMT, BF16, 0>(w[i], c[h]);
-          a[4 * i + 1] = natural_pair<FMT, BF16, 1>(w[i], c[h]);
-          a[4 * i + 2] = natural_pair<FMT, BF16, 2>(w[i], c[h]);
-          a[4 * i + 3] = natural_pair<FMT, BF16, 3>(w[i], c[h]);
-          if constexpr (!C::POST && FMT == MOE_W_MXFP4) {
+          for (int i = 0; i < 8; ++i) {
+            const int h = i * 8 / HK;
+            const uint32_t up = w[i] >> 4;
+            a[4 * i] = natural_pair<FMT, BF16, 0>(w[i], up, c[h]);
+            a[4 * i + 1] = natural_pair<FMT, BF16, 1>(w[i], up, c[h]);
+            a[4 * i + 2] = natural_pair<FMT, BF16, 2>(w[i], up, c[h]);
+            a[4 * i + 3] = natural_pair<FMT, BF16, 3>(w[i], up, c[h]);
+            if constexpr (!C::POST && FMT == MOE_W_MXFP4) {
 #pragma unroll
-            for (int p = 4 * i; p < 4 * i + 4; ++p) a[p] = w4::mul2<true>(a[p], s1[h]);
-          }
-          if constexpr (C::PLANES == 2) {
-            // (code - zero) * scale = hi + lo: hi rounded, lo what is left, exact
+              for (int p = 4 * i; p < 4 * i + 4; ++p) a[p] = w4::mul2<true>(a[p], s1[h]);
+            }
+            if constexpr (C::PLANES == 2) {
+              // (code - zero) * scale = hi + lo: hi rounded, lo what is left, exact.  The
+              // first plane holds -hi (the MMA negates it), which lo's one fused
+              // multiply-add takes as it is.
 #pragma unroll
-            for (int p = 4 * i; p < 4 * i + 4; ++p) {
-              const uint32_t v = a[p];
-              a[p] = w4::mul2<true>(v, s1[h]);
-              lo[p] = fms2(v, s1[h], a[p]);
-              if (P.scale_type != MOE_DT_BF16) lo[p] = fma2(v, s2[h], lo[p]);
+              for (int p = 4 * i; p < 4 * i + 4; ++p) {
+                const uint32_t v = a[p];
+                a[p] = w4::mul2<true>(v, s1[h] ^ 0x80008000u);
+                lo[p] = fma2(v, s1[h], a[p]);
+                if constexpr (decltype(third)::value) lo[p] = fma2(v, s2[h], lo[p]);
+              }
             }
           }
-        }
+        };
+        if (C::PLANES == 2 && P.scale_type != MOE_DT_BF16) expand(std::true_type());
+        else expand(std::false_type());
         if (!wait(&aempty[set], aphase ^ 1u)) {
           ok = false;
           break;
