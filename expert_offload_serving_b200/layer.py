@@ -5,6 +5,11 @@ on a CUDA stream: moe_route_topk -> (moe_cache_fill) -> moe_permute ->
 moe_expert_ffn -> moe_combine_merge.  All arithmetic runs in libmoe's
 kernels; this module only allocates, packs expert blobs with moe_pack_expert
 and sequences the calls.
+
+Beside the routed experts: `SharedExpert` (a dense 4-bit SwiGLU expert that
+every token passes through; its sum enters a layer through the combine's
+host_partial) and, for tuning a layer's router while its experts stay as they
+are, MoeLayer.balance and MoeLayer.router_grad.
 """
 from __future__ import annotations
 
@@ -13,9 +18,10 @@ import time
 
 import torch
 
-from . import (MOE_FFN_ACT_NVFP4, FORMATS, MoeCache, _check, lib, moe_combine_merge, moe_expert_blob_bytes,
-               moe_expert_ffn, moe_expert_ffn_workspace_bytes, moe_host_expert_ffn, moe_pack_expert, moe_permute,
-               moe_permute_scratch_bytes, moe_route_topk, moe_split_misses, shape)
+from . import (LINEAR_FORMATS, MOE_FFN_ACT_NVFP4, FORMATS, MoeCache, _check, lib, moe_balance_loss,
+               moe_balance_loss_workspace_bytes, moe_combine_backward, moe_combine_merge, moe_expert_blob_bytes,
+               moe_expert_ffn, moe_expert_ffn_workspace_bytes, moe_host_expert_ffn, moe_linear_w4, moe_pack_expert,
+               moe_permute, moe_permute_scratch_bytes, moe_route_topk, moe_router_backward, moe_split_misses, shape)
 
 
 def _u8(t: torch.Tensor) -> torch.Tensor:
@@ -98,6 +104,44 @@ class ExpertCache:
         self.handle.close()
 
 
+class SharedExpert:
+    """A dense SwiGLU expert that every token passes through, over 4-bit weights:
+    out (+)= W_d (silu(W_g x) * (W_u x)).
+
+    gate_up: (codes [2I, d/2] uint8, scales, zeros or None), the I gate rows and
+    then the I up rows; down: the same of [d, I].  fmt "int4" (group 32, 64 or
+    128), "mxfp4" or "nvfp4" (tensor_scales = the two fp32 scales).  Two
+    launches; the activations between them are rounded to x's type, which the
+    second product takes."""
+
+    def __init__(self, gate_up, down, fmt="int4", group=128, tensor_scales=(1.0, 1.0), T_max=1,
+                 dtype=torch.bfloat16):
+        self.gate_up, self.down = tuple(gate_up), tuple(down)
+        self.fmt, self.group, self.tensor_scales = fmt, group, tensor_scales
+        if fmt not in LINEAR_FORMATS:
+            raise ValueError(f"fmt={fmt!r}: expected one of {sorted(LINEAR_FORMATS)}")
+        self.I, self.d = self.gate_up[0].shape[0] // 2, self.down[0].shape[0]
+        if self.gate_up[0].shape != (2 * self.I, self.d // 2) or self.down[0].shape != (self.d, self.I // 2):
+            raise ValueError(f"gate_up codes {tuple(self.gate_up[0].shape)} and down codes {tuple(self.down[0].shape)} "
+                             "are not [2I, d/2] and [d, I/2]")
+        dev = self.down[0].device
+        self.a = torch.empty((T_max, self.I), dtype=dtype, device=dev)
+        self.status = torch.zeros((1,), dtype=torch.int32, device=dev)
+
+    def add(self, x, out, accumulate=True, stream=None):
+        """out [T, d] (fp32, or x's type) += the expert of x [T, d], or = with
+        accumulate=False."""
+        T = x.shape[0]
+        if T > self.a.shape[0] or x.dtype != self.a.dtype:
+            raise ValueError(f"x {x.dtype} {tuple(x.shape)}: expected {self.a.dtype} and at most {self.a.shape[0]} tokens")
+        for (codes, scales, zeros), ts, src, dst, swiglu, acc in (
+                (self.gate_up, self.tensor_scales[0], x, self.a[:T], True, False),
+                (self.down, self.tensor_scales[1], self.a[:T], out, False, accumulate)):
+            moe_linear_w4(src, codes, scales, dst, fmt=self.fmt, group=self.group, zeros=zeros, tensor_scale=ts,
+                          swiglu=swiglu, accumulate=acc, dev_status=self.status, stream=stream)
+        return out
+
+
 class MoeLayer:
     """One MoE layer of shape (E, d, I, fmt) with top-k routing.
 
@@ -105,10 +149,11 @@ class MoeLayer:
     Cached mode: `host_pool` (pinned, E blobs) plus `n_slots` device slots
     managed by the LRU cache -- or `cache` (an ExpertCache shared by several
     layers) and this layer's `layer_id` in it; call `prepare(step, experts)`
-    to fill.  act="nvfp4" selects the FP4 tensor-core FFN (fused combine)."""
+    to fill.  act="nvfp4" selects the FP4 tensor-core FFN (fused combine).
+    shared (a SharedExpert with bf16 activations): forward() adds its output."""
 
     def __init__(self, E, d, I, fmt, k, T_max, device="cuda", device_pool=None, host_pool=None,
-                 n_slots=None, act="none", cache=None, layer_id=0):
+                 n_slots=None, act="none", cache=None, layer_id=0, shared=None):
         self.E, self.d, self.I, self.k, self.fmt, self.act = E, d, I, k, fmt, act
         self.s = shape(E, d, I, fmt)
         self.B = moe_expert_blob_bytes(self.s)
@@ -130,6 +175,12 @@ class MoeLayer:
         self.y_perm = None if act == "nvfp4" else torch.empty((max(n, 1), d), **f32)
         self.out = torch.empty((T_max, d), **f32)
         self.status = torch.zeros((1,), **i32)
+        self.shared = shared
+        if shared is not None:
+            if shared.d != d or shared.a.shape[0] < T_max or shared.a.dtype != torch.bfloat16:
+                raise ValueError(f"shared expert of d={shared.d} for {shared.a.shape[0]} {shared.a.dtype} tokens in a "
+                                 f"layer of d={d}, T_max={T_max}")
+            self.shared_out = torch.empty((T_max, d), **f32)
         self.cache = None
         self.xcache = None
         if device_pool is not None:
@@ -329,12 +380,70 @@ class MoeLayer:
                               0 if self.y_perm is None else self.y_perm.data_ptr(), self.flags,
                               self.workspace.data_ptr(), nb(self.workspace))
         s = (torch.cuda.current_stream() if stream is None else stream)
+        if self.shared is not None and T > 0:
+            # the shared expert's sum (and the host's, if there is one) is the partial the combine adds
+            so = self.shared_out[:T]
+            if host_partial is not None:
+                with torch.cuda.stream(torch.cuda.ExternalStream(s) if isinstance(s, int) else s):
+                    so.copy_(host_partial)
+            self.shared.add(x, so, accumulate=host_partial is not None, stream=s)
+            host_partial = so
         s = s if isinstance(s, int) else s.cuda_stream
         hp = 0 if host_partial is None else host_partial.data_ptr()
         _check(lib().moe_layer_forward(self.s, logits.data_ptr(), x.data_ptr(), T, self.k, *self._fwd_args, hp,
                                        self.out.data_ptr(), self.status.data_ptr(), s))
         self._record_reads_done(stream)
         return self.out[:T]
+
+
+    # -- the router's training pass ------------------------------------------------
+    def balance(self, logits, seq_offsets=None, mask=None, stream=None):
+        """The balance loss and statistics of the routing the last forward() (or
+        route()) of these logits left in idx: dict(loss [2], counts [S, E], prob
+        [S, E], coef [S + 1]), new tensors."""
+        T = self._check_T(logits.shape[0])
+        S = 1 if seq_offsets is None else seq_offsets.numel() - 1
+        f32 = dict(dtype=torch.float32, device=self.dev)
+        r = dict(loss=torch.empty((2,), **f32), counts=torch.empty((S, self.E), dtype=torch.int32, device=self.dev),
+                 prob=torch.empty((S, self.E), **f32), coef=torch.empty((S + 1,), **f32))
+        ws = torch.empty((max(1, moe_balance_loss_workspace_bytes(T, self.E, S)),), dtype=torch.uint8, device=self.dev)
+        moe_balance_loss(logits, self.idx[:T], r["loss"], r["counts"], r["prob"], r["coef"], ws,
+                         seq_offsets=seq_offsets, mask=mask, dev_status=self.status, stream=stream)
+        self._keep(stream, ws, *r.values())
+        return r
+
+    def router_grad(self, logits, dout=None, balance=None, dloss=None, seq_offsets=None, mask=None, stream=None):
+        """d(loss)/d(logits) [T, E], the experts held fixed: of the layer's output
+        (dout [T, d], the gradient at forward()'s result; needs y_perm of the last
+        forward, so not act="nvfp4") and of the balance losses (balance: the dict
+        of balance(); dloss [2]: their weights).  Either part may be left out."""
+        T = self._check_T(logits.shape[0])
+        dgate = None
+        if dout is not None:
+            if self.y_perm is None:
+                raise RuntimeError("act='nvfp4' keeps no expert outputs: the gates have no gradient there")
+            self._check_tensor("dout", dout, (T, self.d), torch.float32)
+            dgate = torch.empty((T, self.k), dtype=torch.float32, device=self.dev)
+            moe_combine_backward(self.y_perm, self.idx[:T], self.gate[:T], self.inv_perm, self.slot, dout, self.E, dgate,
+                                 stream=stream)
+            self._record_reads_done(stream)              # it reads the slot table, as combine does
+        if (dloss is None) != (balance is None):
+            raise ValueError("dloss and balance go together")
+        b = balance or {}
+        dlogits = torch.empty((T, self.E), dtype=torch.float32, device=self.dev)
+        moe_router_backward(logits, self.idx[:T], dlogits, gate=self.gate[:T] if dgate is not None else None,
+                            dgate=dgate, counts=b.get("counts"), coef=b.get("coef"), dloss=dloss,
+                            seq_offsets=seq_offsets, mask=mask, dev_status=self.status, stream=stream)
+        self._keep(stream, dlogits, *([] if dgate is None else [dgate]))
+        return dlogits
+
+    def _keep(self, stream, *tensors):
+        """Tensors allocated here and used on a stream of the caller's: their
+        memory is not reused before that stream has passed."""
+        if stream is not None:
+            s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+            for t in tensors:
+                t.record_stream(s)
 
 
 class StreamedPrefill:

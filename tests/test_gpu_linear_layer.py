@@ -1,0 +1,189 @@
+"""The dense 4-bit linear, the balance loss and the gradients where a layer uses
+them: a layer with a shared expert, one router training step of a layer with
+frozen experts, and the bounded-wait path of the tcgen05 linear kernel."""
+import time
+
+import numpy as np
+import pytest
+import torch
+
+import synth
+from oracle import linear as O
+from oracle import moe as M
+from oracle import router as R
+from tests.gpu_util import Built, check_tol, load_moe, require_gpu
+from tests.test_gpu_linear import cuda, make, oracle_weights
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def moe():
+    require_gpu()
+    return load_moe()
+
+
+def shared_expert(fmt, group, d, I, T_max, seed=0):
+    from expert_offload_serving_b200.layer import SharedExpert
+    gu, _ = make(fmt, group, 2 * I, d, 1, zeros=fmt == "int4", seed=seed)
+    dn, _ = make(fmt, group, d, I, 1, zeros=fmt == "int4", seed=seed + 1)
+    if fmt == "nvfp4":
+        gu["tensor_scale"] = dn["tensor_scale"] = 2e-5
+    c, e = cuda(gu), cuda(dn)
+    s = SharedExpert((c["codes"], c["scales"], c["zeros"]), (e["codes"], e["scales"], e["zeros"]), fmt=fmt, group=group,
+                     tensor_scales=(gu["tensor_scale"], dn["tensor_scale"]), T_max=T_max)
+    return s, oracle_weights(gu), oracle_weights(dn)
+
+
+@pytest.mark.parametrize("fmt,group", [("int4", 64), ("mxfp4", 32), ("nvfp4", 16)])
+@pytest.mark.parametrize("T", [1, 6, 40])
+def test_layer_with_a_shared_expert(moe, fmt, group, T):
+    """out = routed experts + shared expert (+ host partial), in one forward()."""
+    cfg = synth.LayerConfig("shared", E=8, k=2, d=512, I=256, fmt="bf16")
+    b = Built(cfg, T, seed=3)
+    ref = b.oracle()["out"]
+    sh, wgu, wd = shared_expert(fmt, group, 512, 192, T)
+    a = O.linear(b.x.double().numpy(), wgu, swiglu=True)
+    a = torch.from_numpy(a).to(torch.bfloat16).double().numpy()        # the activations between the products
+    ref = ref + O.linear(a, wd)
+    from expert_offload_serving_b200.layer import MoeLayer
+    layer = MoeLayer(8, 512, 256, "bf16", 2, T, device_pool=b.layer.pool, shared=sh)
+    layer.slot.copy_(b.layer.slot)
+    out = layer.forward(b.logits.cuda(), b.x.cuda())
+    check_tol(out.cpu().numpy(), ref)
+    hp = torch.randn((T, 512), device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    out = layer.forward(b.logits.cuda(), b.x.cuda(), host_partial=hp, stream=side)
+    side.synchronize()
+    check_tol(out.cpu().numpy(), ref + hp.double().cpu().numpy())
+    moe.moe_check_status(layer.status)
+    moe.moe_check_status(sh.status)
+
+
+def test_shared_expert_refusals(moe):
+    from expert_offload_serving_b200.layer import MoeLayer, SharedExpert
+    sh, _, _ = shared_expert("int4", 64, 512, 192, 4)
+    with pytest.raises(ValueError):
+        sh.add(torch.zeros((5, 512), dtype=torch.bfloat16, device="cuda"), torch.zeros((5, 512), device="cuda"))
+    with pytest.raises(ValueError):
+        sh.add(torch.zeros((2, 512), dtype=torch.float16, device="cuda"), torch.zeros((2, 512), device="cuda"))
+    with pytest.raises(ValueError):
+        SharedExpert(sh.down, sh.gate_up)
+    with pytest.raises(ValueError):
+        SharedExpert(sh.gate_up, sh.down, fmt="bf16")
+    with pytest.raises(ValueError):
+        MoeLayer(8, 256, 256, "bf16", 2, 4, device_pool=torch.empty((8, moe.moe_expert_blob_bytes(
+            moe.shape(8, 256, 256, "bf16"))), dtype=torch.uint8, device="cuda"), shared=sh)
+
+
+@pytest.mark.parametrize("ragged", [False, True])
+def test_router_training_step_with_frozen_experts(moe, ragged):
+    """forward -> balance -> router_grad: the gradient of <dout, out> + dloss . loss
+    with respect to the logits, by the oracle (experts in float64) and against
+    differences of the layer itself."""
+    cfg = synth.LayerConfig("router", E=8, k=2, d=512, I=256, fmt="bf16")
+    T = 24
+    b = Built(cfg, T, seed=4, experts=range(8))
+    logits, x = b.logits.cuda(), b.x.cuda()
+    out = b.layer.forward(logits, x).clone()
+    off = torch.tensor([0, 9, 9, T], dtype=torch.int32, device="cuda") if ragged else None
+    mask = (torch.arange(T, device="cuda") % 5 != 3) if ragged else None
+    bal = b.layer.balance(logits, seq_offsets=off, mask=mask)
+    dloss = torch.tensor([0.05, 0.01], device="cuda")
+    dout = torch.randn((T, 512), device="cuda") * 0.1
+    if mask is not None:
+        dout[~mask] = 0
+    got = b.layer.router_grad(logits, dout, bal, dloss, seq_offsets=off, mask=mask)
+    moe.moe_check_status(b.layer.status)
+
+    idx, gate = M.route_topk(b.logits.numpy(), 2)
+    y = M.per_pair_outputs(b.x.double().numpy(), b.logits.numpy(), 2, b.weights)
+    dg = np.einsum("td,tjd->tj", dout.double().cpu().numpy(), np.asarray(y).reshape(T, 2, 512))
+    o = None if off is None else off.tolist()
+    m = None if mask is None else mask.cpu().numpy()
+    _, counts, _, coef = R.balance(b.logits.numpy(), idx, o, m)
+    assert np.array_equal(bal["counts"].cpu().numpy(), counts)
+    ref = R.router_backward(b.logits.numpy(), idx, gate, dg, counts, coef, dloss.tolist(), o, m)
+    check_tol(got.cpu().numpy(), ref, 1e-4, 1e-5)
+
+    # differences: the routing must not change, so move within the gaps of the top-2
+    v = torch.sign(got)
+    srt = torch.sort(logits, dim=1, descending=True).values
+    h = min(2.0 ** -4, float((srt[:, :2] - srt[:, 1:3]).min()) / 4)
+
+    def value(l):
+        r = b.layer.forward(l, x)
+        q = b.layer.balance(l, seq_offsets=off, mask=mask)
+        return float((r.double() * dout.double()).sum() + (q["loss"].double() * dloss.double()).sum())
+    change = (value(logits + h * v) - value(logits - h * v)) / (2 * h)
+    want = float((got.double() * v).sum())
+    assert torch.equal(b.layer.forward(logits, x), out)
+    # the values are sums of ~1e4 fp32 products of 1e-2: 1e-6 of rounding, over 2h >= 1e-4
+    assert abs(change - want) <= 2e-2 * abs(want) + 1e-2 * h
+
+
+def test_router_grad_parts_and_refusals(moe):
+    cfg = synth.LayerConfig("router", E=8, k=2, d=512, I=256, fmt="bf16")
+    b = Built(cfg, 6, seed=5)
+    logits = b.logits.cuda()
+    b.layer.forward(logits, b.x.cuda())
+    bal = b.layer.balance(logits)
+    dout, dloss = torch.randn((6, 512), device="cuda"), torch.ones(2, device="cuda")
+    both = b.layer.router_grad(logits, dout, bal, dloss)
+    apart = b.layer.router_grad(logits, dout) + b.layer.router_grad(logits, balance=bal, dloss=dloss)
+    assert torch.allclose(both, apart, rtol=1e-5, atol=1e-6)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    again = b.layer.router_grad(logits, dout, b.layer.balance(logits, stream=side), dloss, stream=side)
+    side.synchronize()
+    assert torch.equal(both, again)
+    with pytest.raises(ValueError):
+        b.layer.router_grad(logits, dout, bal)
+    with pytest.raises(ValueError):
+        b.layer.router_grad(logits, dout[:, :256])
+    nv = Built(synth.LayerConfig("nv", E=8, k=2, d=512, I=256, fmt="nvfp4", act="nvfp4"), 6, seed=6, act="nvfp4")
+    nv.run()
+    with pytest.raises(RuntimeError):
+        nv.layer.router_grad(nv.logits.cuda(), dout)
+    assert torch.isfinite(nv.layer.router_grad(nv.logits.cuda(), balance=nv.layer.balance(nv.logits.cuda()),
+                                               dloss=dloss)).all()
+
+
+@pytest.mark.parametrize("T", [24, 300])
+def test_wait_expiry_of_the_linear_is_reported(moe, T):
+    """With the testing aids on, CTA 0's workers wait on a barrier nothing arrives
+    on: the call reports MOE_ERR_TIMEOUT, and the next one is right again."""
+    w, x = make("int4", 128, 256, 2048, T, zeros=True, seed=13)
+    d, xs = cuda(w), x.cuda()
+    out, st = torch.empty((T, 256), device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    args = dict(fmt="int4", group=128, zeros=d["zeros"], dev_status=st)
+    prev = moe.moe_set_wait_limit_ns(5_000_000)
+    moe.moe_set_test_stall(True)
+    try:
+        t0 = time.perf_counter()
+        moe.moe_linear_w4(xs, d["codes"], d["scales"], out, **args)
+        with pytest.raises(moe.MoeError) as e:
+            moe.moe_check_status(st)
+        assert e.value.status == moe.MOE_ERR_TIMEOUT and time.perf_counter() - t0 < 30
+    finally:
+        moe.moe_set_test_stall(False)
+        moe.moe_set_wait_limit_ns(prev)
+    for _ in range(2):
+        moe.moe_linear_w4(xs, d["codes"], d["scales"], out, **args)
+        moe.moe_check_status(st)
+        check_tol(out.cpu().numpy(), O.linear(x.double().numpy(), oracle_weights(w)), 1e-4, 1e-5)
+
+
+@pytest.mark.parametrize("path", ["warp", "tc"])
+@pytest.mark.parametrize("fmt,group", [("int4", 32), ("int4", 128), ("mxfp4", 32), ("nvfp4", 16)])
+def test_both_kernels_at_every_token_count(moe, monkeypatch, path, fmt, group):
+    """MOE_LINEAR forces a kernel where the rule would take the other."""
+    from tests.test_gpu_linear import DT, call, check
+    monkeypatch.setenv("MOE_LINEAR", path)
+    for T in (1, 3, 16, 17, 31, 64, 65, 129, 257):
+        for x in ("bf16", "f16"):
+            w, xs = make(fmt, group, 200, 1056, T, x=x, zeros=fmt == "int4", seed=14)
+            out = torch.empty((T, 200), dtype=DT["f32"], device="cuda")
+            call(moe, cuda(w), xs.cuda(), out)
+            check(out, w, xs, "f32")
