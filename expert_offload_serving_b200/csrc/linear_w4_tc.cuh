@@ -558,7 +558,6 @@ cudaError_t launch(const LinearParams& P, const DeviceInfo& dev, int32_t* status
 
 template <int FMT, int GROUP, bool BF16>
 cudaError_t launch_tokens(const LinearParams& P, const DeviceInfo& dev, int32_t* status, cudaStream_t s) {
-  if (P.T <= 16) return launch<FMT, GROUP, BF16, 16>(P, dev, status, s);
   if (P.T <= 32) return launch<FMT, GROUP, BF16, 32>(P, dev, status, s);
   if (P.T <= 64) return launch<FMT, GROUP, BF16, 64>(P, dev, status, s);
   return launch<FMT, GROUP, BF16, 128>(P, dev, status, s);

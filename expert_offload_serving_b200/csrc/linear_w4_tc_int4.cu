@@ -1,17 +1,27 @@
-// The dense 4-bit linear over INT4 weights on the 5th-generation tensor cores (linear_w4_tc.cuh).
-#include "linear_w4_tc.cuh"
+// The dense 4-bit linear over INT4 weights on the 5th-generation tensor cores (linear_w4_tc.cuh,
+// linear_w4_tc16.cuh).
+#include "linear_w4_tc16.cuh"
 
 namespace moe {
+namespace {
+
+template <int FMT, int GROUP, bool BF16>
+cudaError_t launch(const LinearParams& P, const DeviceInfo& dev, int32_t* status, cudaStream_t s) {
+  return P.T <= w4t16::NT ? w4t16::launch<FMT, GROUP, BF16>(P, dev, status, s)
+                          : w4tc::launch_tokens<FMT, GROUP, BF16>(P, dev, status, s);
+}
+
+}  // namespace
 
 cudaError_t launch_linear_tc_int4(const LinearParams& P, int group, bool bf16, const DeviceInfo& dev, int32_t* status,
                                  cudaStream_t s) {
   switch (group) {
-    case 32: return bf16 ? w4tc::launch_tokens<MOE_W_INT4, 32, true>(P, dev, status, s)
-                         : w4tc::launch_tokens<MOE_W_INT4, 32, false>(P, dev, status, s);
-    case 64: return bf16 ? w4tc::launch_tokens<MOE_W_INT4, 64, true>(P, dev, status, s)
-                         : w4tc::launch_tokens<MOE_W_INT4, 64, false>(P, dev, status, s);
-    default: return bf16 ? w4tc::launch_tokens<MOE_W_INT4, 128, true>(P, dev, status, s)
-                         : w4tc::launch_tokens<MOE_W_INT4, 128, false>(P, dev, status, s);
+    case 32: return bf16 ? launch<MOE_W_INT4, 32, true>(P, dev, status, s)
+                         : launch<MOE_W_INT4, 32, false>(P, dev, status, s);
+    case 64: return bf16 ? launch<MOE_W_INT4, 64, true>(P, dev, status, s)
+                         : launch<MOE_W_INT4, 64, false>(P, dev, status, s);
+    default: return bf16 ? launch<MOE_W_INT4, 128, true>(P, dev, status, s)
+                         : launch<MOE_W_INT4, 128, false>(P, dev, status, s);
   }
 }
 
