@@ -4,6 +4,31 @@
 
 #include "linear_w4.cuh"
 
+namespace moe {
+namespace {
+
+// Which kernel: warp-level MMAs (linear_w4.cuh) or tcgen05 (linear_w4_tc.cuh,
+// linear_w4_tc16.cuh).  A tcgen05 tile of 128 rows is a chain of stages that takes
+// some 0.5 to 1 us a 1024 of K however few tokens it serves; many tokens, or enough
+// tiles to fill the SMs, pay for it.  Device time in us, warp / tcgen05, K = 4096:
+//   T = 8    N = 16384   INT4/128 15.3 / 17.4   MXFP4 24.8 / 26.2   NVFP4 23.0 / 30.3
+//   T = 16   N = 16384   INT4/128 23.8 / 17.7   INT4/32 28.3 / 29.2  MXFP4 30.5 / 26.3  NVFP4 27.8 / 30.3
+//            N = 131072  INT4/128  150 / 113    INT4/32  195 / 195   MXFP4  205 / 170   NVFP4  188 / 195
+//   T = 32   N = 4096    INT4/128 18.3 / 21.8   INT4/32 23.9 / 29.6  MXFP4 22.9 / 23.5  NVFP4 19.7 / 27.3
+//            N = 16384   INT4/128 27.6 / 22.2   INT4/32 43.8 / 30.0  MXFP4 44.5 / 24.1  NVFP4 38.7 / 27.7
+// MOE_LINEAR=warp|tc, read at every call, forces one.
+bool use_tc(const LinearParams& P, int fmt, int group, const DeviceInfo& dev) {
+  const char* force = getenv("MOE_LINEAR");
+  if (force != nullptr) return strcmp(force, "tc") == 0;
+  if (P.T > 32) return true;
+  const bool fills = P.N >= 77 * dev.sm_count;                 // 0.6 tiles of 128 rows for each SM
+  if (P.T > 16) return fills;
+  return P.T > 8 && fills && (fmt == MOE_W_MXFP4 || (fmt == MOE_W_INT4 && group >= 64));
+}
+
+}  // namespace
+}  // namespace moe
+
 using namespace moe;
 
 extern "C" moe_status moe_linear_w4(moe_linear_shape s, const void* codes, const void* scales, const uint8_t* zeros,
@@ -56,8 +81,7 @@ extern "C" moe_status moe_linear_w4(moe_linear_shape s, const void* codes, const
   P.accumulate = (flags & MOE_LINEAR_ACCUMULATE) != 0;
   P.tensor_scale = tensor_scale;
   const bool bf16 = x_type == MOE_DT_BF16;
-  const char* force = getenv("MOE_LINEAR");
-  const bool tc = force != nullptr ? strcmp(force, "tc") == 0 : T > 16;
+  const bool tc = use_tc(P, s.fmt, s.group, dev);
   const cudaError_t e = tc ? (int4 ? launch_linear_tc_int4(P, s.group, bf16, dev, dev_status, stream)
                                    : launch_linear_tc_fp4(P, s.fmt, bf16, dev, dev_status, stream))
                            : (int4 ? launch_linear_int4(P, s.group, bf16, dev, stream)

@@ -27,6 +27,8 @@
 // each, so that a thread's accumulators hold h and u of one output.
 #pragma once
 
+#include <type_traits>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -48,6 +50,7 @@ struct LinearParams {
   int wm_bits;             // warps along the rows (log2); the warps left over split K
   int stages, ring;        // stages in flight + 1; slots (no more than there are stages)
   int x_rows;              // token rows a stage holds
+  int scale_vec;           // a thread's scales (and zeros) of a stage can be loaded at once
 };
 
 // Launchers, one per format family (linear_w4_int4.cu, linear_w4_fp4.cu).
@@ -182,30 +185,41 @@ __device__ __forceinline__ void store_y(const LinearParams& P, int t, int n, flo
   }
 }
 
-// GROUP: elements of K per scale; NT, RT: 8-token and 16-row tiles of a warp; WN:
-// warps along the tokens.
-template <int FMT, int GROUP, bool BF16, int NT, int RT, int WN>
+// GROUP: elements of K per scale; NT, RT: 8-token and 16-row tiles of a warp.
+template <int FMT, int GROUP, bool BF16, int NT, int RT>
 struct Geometry {
-  static constexpr int KW = NT == 8 ? 128 : 256;                        // K a warp takes from a stage
-  static constexpr int STAGE_WEIGHTS = 8 / WN * 16 * RT * KW;
-  static constexpr int SCALES = STAGE_WEIGHTS / GROUP;
-  static constexpr int EPT = SCALES < kThreads ? 1 : SCALES / kThreads; // scales a thread fetches per stage
+  static constexpr int KW = 256;                                        // K a warp takes from a stage
+  static constexpr int STAGE_WEIGHTS = 8 * 16 * RT * KW;
+  static constexpr int EPT = STAGE_WEIGHTS / GROUP / kThreads;          // scales a thread fetches per stage
   static constexpr int CPT = STAGE_WEIGHTS / 32 / kThreads;             // 16-byte chunks of codes a thread copies
   static constexpr int ENTRY = FMT == MOE_W_INT4 ? 8 : 4;               // bytes of a scale in shared memory
+  // a 16-bit INT4 scale or a scale byte in global memory; EPT of them, EPT zeros
+  using Elem = typename std::conditional<FMT == MOE_W_INT4, uint16_t, uint8_t>::type;
+  static constexpr int VB = EPT * sizeof(Elem);
+  template <int B>
+  using Bytes = typename std::conditional<
+      B == 1, uint8_t,
+      typename std::conditional<
+          B == 2, uint16_t,
+          typename std::conditional<B == 4, uint32_t,
+                                    typename std::conditional<B == 8, uint2, uint4>::type>::type>::type>::type;
+  using Vec = Bytes<VB>;
+  using ZVec = Bytes<EPT>;
+  static_assert(VB <= 16, "one load");
   static_assert(CPT >= 2, "a thread copies rows of both parts");
   int wk, ks, m, gps, cpitch, xpitch, spitch, stage, sbuf, zero_at, s_at, bytes;
   // wk: warps along K; ks: K per stage; m: rows; gps: groups of a row per stage;
   // pitches: bytes of a row of codes (conflict-free 4-byte reads of 8 rows), of x
-  // (16-byte reads of 2 rows) and of scales (odd in entries)
-  static constexpr int TOKENS = 8 * NT * WN;
+  // (16-byte reads of 2 rows) and of scales (8 rows apart, 16-byte writes)
+  static constexpr int TOKENS = 8 * NT;
   __host__ __device__ explicit Geometry(const LinearParams& P) {
-    wk = (8 / WN) >> P.wm_bits;
+    wk = 8 >> P.wm_bits;
     ks = KW * wk;
     m = 16 * RT << P.wm_bits;
     gps = ks / GROUP;
     cpitch = ks / 2 + 16;
     xpitch = ks * 2 + 64;
-    spitch = (gps + 1) * ENTRY;
+    spitch = gps * ENTRY + 16;
     stage = m * cpitch + P.x_rows * xpitch;
     sbuf = (m * spitch + 15) / 16 * 16;
     zero_at = P.ring * stage;                 // one row of zeros for the tokens that are not there
@@ -214,17 +228,16 @@ struct Geometry {
   }
 };
 
-template <int FMT, int GROUP, bool BF16, int NT, int RT, int WN>
-__global__ void __launch_bounds__(kThreads, NT < 8 ? 2 : 1) linear_w4_kernel(const __grid_constant__ LinearParams P) {
-  using G = Geometry<FMT, GROUP, BF16, NT, RT, WN>;
+template <int FMT, int GROUP, bool BF16, int NT, int RT>
+__global__ void __launch_bounds__(kThreads, 2) linear_w4_kernel(const __grid_constant__ LinearParams P) {
+  using G = Geometry<FMT, GROUP, BF16, NT, RT>;
   constexpr int KW = G::KW, KB = KW / 32, GB = GROUP >= 32 ? GROUP / 32 : 1;
   constexpr bool PERMUTE = FMT == MOE_W_INT4 || BF16;                // x pairs (k, k+4): see pair_of
   extern __shared__ __align__(16) unsigned char smem[];
   const G geo(P);
   const uint32_t sm = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
-  const int wm = warp & ((1 << P.wm_bits) - 1), wn = WN == 1 ? 0 : (warp >> P.wm_bits) & (WN - 1);
-  const int wk = warp >> P.wm_bits >> (WN - 1);                      // WN is 1 or 2
+  const int wm = warp & ((1 << P.wm_bits) - 1), wk = warp >> P.wm_bits;
   const int tok0 = blockIdx.y * G::TOKENS;
   const int x_rows = min(P.x_rows, P.T - tok0);
   const int nst = (P.K + geo.ks - 1) / geo.ks;
@@ -279,54 +292,76 @@ __global__ void __launch_bounds__(kThreads, NT < 8 ? 2 : 1) linear_w4_kernel(con
   };
   for (int i = 0; i < P.stages - 1; ++i) issue(i);
 
-  // Scales of a stage: thread -> group `sg` of every s_rows-th row; raw values in registers.
-  const int gps_bits = 31 - __clz(geo.gps), sg = tid & (geo.gps - 1);
-  const int s_rows = kThreads >> gps_bits, s_r = tid >> gps_bits;
-  constexpr int EH = G::EPT > 1 ? G::EPT / 2 : 1;
-  size_t ssrc[2];
-  unsigned sok = 0;
-#pragma unroll
-  for (int i = 0; i < G::EPT; ++i) sok |= (s_r < geo.m && there(i * s_rows + s_r)) << i;
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-    ssrc[h] = static_cast<size_t>(row_of(min(h * EH * s_rows + s_r, geo.m - 1))) * P.groups + sg;
-  const size_t sstep = static_cast<size_t>(s_rows) * P.groups;
+  // Scales of a stage: a thread takes EPT consecutive groups of one row, in one
+  // load where rows are aligned for that (P.scale_vec), as raw values in registers.
+  using E = typename G::Elem;
+  const int tpr_bits = 31 - __clz(geo.gps / G::EPT);                 // threads of a row
+  const int s_r = tid >> tpr_bits, sg = (tid & ((1 << tpr_bits) - 1)) * G::EPT;
+  const bool s_ok = there(s_r);
+  const size_t ssrc = static_cast<size_t>(row_of(s_r)) * P.groups + sg;
   uint32_t sraw[G::EPT], zraw[G::EPT];
   auto fetch = [&](int st) {
-    const int j = st * geo.gps;
-    const bool in = j + sg < P.groups;
+    const int j = st * geo.gps + sg;                                 // first group
+    const size_t at = ssrc + st * geo.gps;
 #pragma unroll
     for (int i = 0; i < G::EPT; ++i) {
       sraw[i] = 0;
       zraw[i] = 8;
-      if (in && (sok >> i & 1)) {
-        const size_t at = ssrc[i / EH] + j + i % EH * sstep;
-        if constexpr (FMT == MOE_W_INT4) {
-          sraw[i] = P.scale_type == MOE_DT_F32 ? __ldg(static_cast<const uint32_t*>(P.scales) + at)
-                                               : __ldg(static_cast<const uint16_t*>(P.scales) + at);
-          if (P.zeros != nullptr) zraw[i] = __ldg(P.zeros + at) & 15u;
-        } else {
-          sraw[i] = 0x100u | __ldg(static_cast<const uint8_t*>(P.scales) + at);   // 0x100: there is one
-        }
+    }
+    if (!s_ok || j >= P.groups) return;
+    if (P.scale_vec && j + G::EPT <= P.groups) {
+      if (FMT == MOE_W_INT4 && P.scale_type == MOE_DT_F32) {
+#pragma unroll
+        for (int i = 0; i < G::EPT; ++i) sraw[i] = __ldg(static_cast<const uint32_t*>(P.scales) + at + i);
+      } else {
+        union { typename G::Vec v; E e[G::EPT]; } u;
+        u.v = __ldg(reinterpret_cast<const typename G::Vec*>(static_cast<const E*>(P.scales) + at));
+#pragma unroll
+        for (int i = 0; i < G::EPT; ++i) sraw[i] = FMT == MOE_W_INT4 ? u.e[i] : 0x100u | u.e[i];   // 0x100: there is one
+      }
+      if (FMT == MOE_W_INT4 && P.zeros != nullptr) {
+        union { typename G::ZVec v; uint8_t e[G::EPT]; } u;
+        u.v = __ldg(reinterpret_cast<const typename G::ZVec*>(P.zeros + at));
+#pragma unroll
+        for (int i = 0; i < G::EPT; ++i) zraw[i] = u.e[i] & 15u;
+      }
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < G::EPT; ++i) {
+      if (j + i >= P.groups) break;
+      if constexpr (FMT == MOE_W_INT4) {
+        sraw[i] = P.scale_type == MOE_DT_F32 ? __ldg(static_cast<const uint32_t*>(P.scales) + at + i)
+                                             : __ldg(static_cast<const uint16_t*>(P.scales) + at + i);
+        if (P.zeros != nullptr) zraw[i] = __ldg(P.zeros + at + i) & 15u;
+      } else {
+        sraw[i] = 0x100u | __ldg(static_cast<const uint8_t*>(P.scales) + at + i);
       }
     }
   };
   unsigned char* const sdst = smem + geo.s_at + s_r * geo.spitch + sg * G::ENTRY;
   auto put = [&](int st) {
-    unsigned char* d = sdst + (st & 1) * geo.sbuf;
-    if (G::SCALES < kThreads && s_r >= geo.m) return;
+    uint32_t v[G::EPT * G::ENTRY / 4];
 #pragma unroll
-    for (int i = 0; i < G::EPT; ++i, d += s_rows * geo.spitch) {
+    for (int i = 0; i < G::EPT; ++i) {
       if constexpr (FMT == MOE_W_INT4) {
-        const uint32_t f = P.scale_type == MOE_DT_F32    ? sraw[i]
-                           : P.scale_type == MOE_DT_BF16 ? sraw[i] << 16
-                                                         : __float_as_uint(__half2float(__ushort_as_half(sraw[i])));
-        *reinterpret_cast<uint2*>(d) = make_uint2(f, ((BF16 ? 0x4300u : 0x6400u) | zraw[i]) * 0x10001u);
+        v[2 * i] = P.scale_type == MOE_DT_F32    ? sraw[i]
+                   : P.scale_type == MOE_DT_BF16 ? sraw[i] << 16
+                                                 : __float_as_uint(__half2float(__ushort_as_half(sraw[i])));
+        v[2 * i + 1] = ((BF16 ? 0x4300u : 0x6400u) | zraw[i]) * 0x10001u;
       } else if constexpr (FMT == MOE_W_MXFP4) {
-        *reinterpret_cast<float*>(d) = sraw[i] == 0 ? 0.f : e8m0_value(sraw[i] & 255u);
+        v[i] = sraw[i] == 0 ? 0u : __float_as_uint(e8m0_value(sraw[i] & 255u));
       } else {
-        *reinterpret_cast<uint32_t*>(d) = sraw[i] == 0 ? 0u : e4m3_mult<BF16>(sraw[i] & 255u);
+        v[i] = sraw[i] == 0 ? 0u : e4m3_mult<BF16>(sraw[i] & 255u);
       }
+    }
+    unsigned char* d = sdst + (st & 1) * geo.sbuf;
+    if constexpr (G::EPT * G::ENTRY == 8) {
+      *reinterpret_cast<uint2*>(d) = make_uint2(v[0], v[1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < G::EPT * G::ENTRY / 4; i += 4)
+        *reinterpret_cast<uint4*>(d + i * 4) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
     }
   };
   fetch(0);
@@ -348,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, NT < 8 ? 2 : 1) linear_w4_kernel(con
   const uint32_t code_at = row * geo.cpitch + wk * (KW / 2) + t4 * 4;
   const uint32_t scale_at = geo.s_at + row * geo.spitch +
                             (wk * (KW / GROUP) + (FMT == MOE_W_NVFP4 ? t4 >> 1 : 0)) * G::ENTRY;
-  const uint32_t x_at = geo.m * geo.cpitch + (wn * 8 * NT + g) * geo.xpitch + wk * (KW * 2) + t4 * 16;
+  const uint32_t x_at = geo.m * geo.cpitch + g * geo.xpitch + wk * (KW * 2) + t4 * 16;
   int slot = 0;
   for (int st = 0; st < nst; ++st) {
     cp_wait(P.stages - 2);
@@ -363,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, NT < 8 ? 2 : 1) linear_w4_kernel(con
     uint32_t xa[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
-      xa[nt] = wn * 8 * NT + nt * 8 + g < x_rows ? at + x_at + nt * 8 * geo.xpitch : geo.zero_at + t4 * 16;
+      xa[nt] = nt * 8 + g < x_rows ? at + x_at + nt * 8 * geo.xpitch : geo.zero_at + t4 * 16;
     uint32_t c[2 * RT];
     float f[2 * RT];
 #pragma unroll
@@ -456,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, NT < 8 ? 2 : 1) linear_w4_kernel(con
   for (int rt = 0; rt < RT; ++rt) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int t = tok0 + (wn * NT + nt) * 8 + t4 * 2, r = row + rt * rt_step;
+      const int t = tok0 + nt * 8 + t4 * 2, r = row + rt * rt_step;
       const float (&v)[4] = acc[rt][nt];
       if (P.swiglu) {
 #pragma unroll
@@ -473,10 +508,10 @@ __global__ void __launch_bounds__(kThreads, NT < 8 ? 2 : 1) linear_w4_kernel(con
 
 constexpr int kSmemMax = 227 * 1024;
 
-template <int FMT, int GROUP, bool BF16, int NT, int RT, int WN>
+template <int FMT, int GROUP, bool BF16, int NT, int RT>
 cudaError_t launch(LinearParams P, const DeviceInfo& dev, cudaStream_t s) {
-  using G = Geometry<FMT, GROUP, BF16, NT, RT, WN>;
-  auto kern = linear_w4_kernel<FMT, GROUP, BF16, NT, RT, WN>;
+  using G = Geometry<FMT, GROUP, BF16, NT, RT>;
+  auto kern = linear_w4_kernel<FMT, GROUP, BF16, NT, RT>;
   static bool done[64] = {};
   if (!done[dev.id]) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
@@ -488,8 +523,9 @@ cudaError_t launch(LinearParams P, const DeviceInfo& dev, cudaStream_t s) {
   // rows mean more warps along K and a longer stage of x, so not so few that a
   // stage is longer than K or its x more than twice its codes.
   P.x_rows = P.T < G::TOKENS ? P.T : G::TOKENS;
-  P.wm_bits = NT < 8 ? 3 : 2;
-  while (NT < 8 && P.wm_bits > 0 && (tiles / RT >> P.wm_bits) * 2 < dev.sm_count * 3) {
+  P.scale_vec = P.groups % G::EPT == 0 && aligned(P.scales, G::VB) && aligned(P.zeros, G::EPT);
+  P.wm_bits = 3;
+  while (P.wm_bits > 0 && (tiles / RT >> P.wm_bits) * 2 < dev.sm_count * 3) {
     LinearParams q = P;
     --q.wm_bits;
     q.ring = 2;
@@ -505,7 +541,7 @@ cudaError_t launch(LinearParams P, const DeviceInfo& dev, cudaStream_t s) {
   const int per = P.swiglu ? geo.m / 2 : geo.m, outs = P.swiglu ? P.N / 2 : P.N;
   const dim3 grid((outs + per - 1) / per, (P.T + G::TOKENS - 1) / G::TOKENS);
   // As deep a ring as lets two CTAs share an SM, or one where one is all there is.
-  const bool two = NT < 8 && static_cast<int64_t>(grid.x) * grid.y > dev.sm_count;
+  const bool two = static_cast<int64_t>(grid.x) * grid.y > dev.sm_count;
   for (int n = 3; n <= kMaxStages && n <= nst + 1; ++n) {
     LinearParams q = P;
     q.stages = n;
@@ -520,19 +556,17 @@ cudaError_t launch(LinearParams P, const DeviceInfo& dev, cudaStream_t s) {
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// Tokens per warp: NT tiles of 8.  A warp takes 32 rows (RT = 2), so that x is
-// read from shared memory and permuted once for two row tiles, unless that leaves
-// SMs without a CTA.
+// Tokens per warp: NT tiles of 8 (above 32 tokens the grid's second dimension takes
+// 32 each).  Up to 16 tokens a warp takes 32 rows (RT = 2) where that leaves every
+// SM two CTAs, so that x is read from shared memory and permuted once for two row
+// tiles: 20 % fewer instructions, though measured about even (T = 13, N = 128001,
+// K = 4096, groups of 64: 155.6 against 155.4 us).
 template <int FMT, int GROUP, bool BF16>
 cudaError_t launch_tokens(const LinearParams& P, const DeviceInfo& dev, cudaStream_t s) {
   const bool wide = P.N >= 64 * dev.sm_count;
-  if (P.T <= 8)
-    return wide ? launch<FMT, GROUP, BF16, 1, 2, 1>(P, dev, s) : launch<FMT, GROUP, BF16, 1, 1, 1>(P, dev, s);
-  if (P.T <= 16)
-    return wide ? launch<FMT, GROUP, BF16, 2, 2, 1>(P, dev, s) : launch<FMT, GROUP, BF16, 2, 1, 1>(P, dev, s);
-  if (P.T <= 32) return launch<FMT, GROUP, BF16, 4, 1, 1>(P, dev, s);
-  if (P.T <= 64) return launch<FMT, GROUP, BF16, 8, 2, 1>(P, dev, s);
-  return launch<FMT, GROUP, BF16, 8, 2, 2>(P, dev, s);
+  if (P.T <= 8) return wide ? launch<FMT, GROUP, BF16, 1, 2>(P, dev, s) : launch<FMT, GROUP, BF16, 1, 1>(P, dev, s);
+  if (P.T <= 16) return wide ? launch<FMT, GROUP, BF16, 2, 2>(P, dev, s) : launch<FMT, GROUP, BF16, 2, 1>(P, dev, s);
+  return launch<FMT, GROUP, BF16, 4, 1>(P, dev, s);
 }
 
 }  // namespace w4

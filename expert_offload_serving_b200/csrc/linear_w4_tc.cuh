@@ -125,13 +125,15 @@ __device__ __forceinline__ void tmem_load(uint32_t taddr, float (&v)[N]) {
   else tmem_ld32(taddr, v);
 }
 
-// A bounded wait for hand-overs that are due within a stage.  The plain try_wait
-// suspends the thread in hardware for a while and wakes it at once; the form with
-// a time hint sleeps in coarse steps, which cost more than a stage each.  The
-// clock is read only after 64 looks in vain: reading it takes some 400 cycles.
+// A bounded wait for hand-overs that are due within a stage.  A look in vain is
+// followed by a short sleep: waiting warps that look without pause took a third of
+// the issue slots from those that work.  The clock is read only after 64 looks:
+// reading it takes some 400 cycles, as long as a stage should.
 __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint64_t limit_ns) {
-  for (int i = 0; i < 64; ++i)
+  for (int i = 0; i < 64; ++i) {
     if (mbar_try(bar, parity)) return true;
+    __nanosleep(20);
+  }
   return mbar_wait<false>(bar, parity, abort_flag, limit_ns);
 }
 

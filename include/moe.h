@@ -451,10 +451,13 @@ moe_status moe_profile_bandwidth(moe_shape s, const void* host_pool, int n_blobs
  *            values silu(h) * u.  With MOE_LINEAR_ACCUMULATE y += instead.
  *            Elements of y outside these rows are left as they were; y may not
  *            overlap x or the weights.
- * Products are exact, sums are fp32 in a fixed order (the same call gives the
- * same bits), y is rounded once.  dev_status: device int32 word or NULL;
- * MOE_ERR_TIMEOUT is recorded there if a bounded wait of the tcgen05 kernel runs
- * out (y is then incomplete).  x, scales, codes and y: codes and x 16-byte
+ * Products are exact (with bf16 x and INT4 scales in fp16 or fp32, within 2^-16 of
+ * the weight on the tcgen05 kernels), sums are fp32 in a fixed order (the same call
+ * gives the same bits), y is rounded once.  dev_status: device int32 word or NULL;
+ * MOE_ERR_TIMEOUT is recorded there if a bounded wait of the tcgen05 kernels runs
+ * out (y is then incomplete).  Warp-level or tcgen05 kernels are chosen by T, N and
+ * the format; the environment variable MOE_LINEAR=warp|tc, read at every call,
+ * forces one.  x, scales, codes and y: codes and x 16-byte
  * aligned, y and scales aligned to their element.  T >= 0 (T = 0 enqueues
  * nothing), T <= 1 << 20. */
 typedef enum moe_dtype { MOE_DT_F32 = 0, MOE_DT_BF16 = 1, MOE_DT_F16 = 2 } moe_dtype;
