@@ -20,9 +20,8 @@ namespace {
 bool use_tc(const LinearParams& P, int fmt, int group, const DeviceInfo& dev) {
   const char* force = getenv("MOE_LINEAR");
   if (force != nullptr) return strcmp(force, "tc") == 0;
-  if (P.T > 32) return true;
+  if (P.T > 16) return true;
   const bool fills = P.N >= 77 * dev.sm_count;                 // 0.6 tiles of 128 rows for each SM
-  if (P.T > 16) return fills;
   return P.T > 8 && fills && (fmt == MOE_W_MXFP4 || (fmt == MOE_W_INT4 && group >= 64));
 }
 

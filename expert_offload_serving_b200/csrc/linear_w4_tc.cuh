@@ -20,6 +20,10 @@
 // takes cost more than the second plane: at T = 64, N = 16384, K = 4096 with groups
 // of 128, POST took 25 us in bf16.
 //
+// Few tiles: a cluster of 2, 4 or 8 CTAs shares a tile, each with a part of K, and
+// each adds up, out of the others' shared memory and in their order, the sums of a
+// part of the tokens.
+//
 // Two sets of eight warps take the stages in turn, each with its own A buffer,
 // accumulators and MMA-issuing warp: the hand-overs of a stage (codes landed ->
 // expanded -> multiplied -> added up) cost more time than its work, and the sets'
@@ -55,6 +59,7 @@ struct TcParams {
   LinearParams L;
   uint64_t wait_ns;
   int stall, mt, tt;                          // tiles of rows, of tokens
+  int ck_bits;                                // CTAs of a cluster that share a tile's K (log2)
   int32_t* status;
 };
 
@@ -72,6 +77,7 @@ struct Cfg {
   static constexpr int BAR_BYTES = (N_BARS * 8 + 16 + 127) / 128 * 128;
   static constexpr int SMEM = 1024 + S * STAGE + BAR_BYTES;
   static_assert(SMEM <= 227 * 1024, "shared memory");
+  static_assert(kWorkers * 32 * NT <= S * STAGE, "the sums of a CTA fit the stages' memory");
   static_assert(STAGE % 1024 == 0 && S >= 3 && ND >= 1, "");
 };
 
@@ -157,7 +163,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + C::N_BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int nst = (P.K + KS - 1) / KS, ntiles = Q.mt * Q.tt;
+  // this CTA's stages of K: nst of them from s0 on (all, but for a shared tile)
+  const int ck = 1 << Q.ck_bits, rank = Q.ck_bits == 0 ? 0 : static_cast<int>(cluster_rank());
+  const int all = (P.K + KS - 1) / KS, s0 = all * rank >> Q.ck_bits, nst = (all * (rank + 1) >> Q.ck_bits) - s0;
+  const int ntiles = Q.mt * Q.tt, tile0 = blockIdx.x >> Q.ck_bits, tiles_step = gridDim.x >> Q.ck_bits;
+  int meetings = 0;                           // barriers over the cluster: two, on every path
   const int outs = P.swiglu ? P.N >> 1 : P.N, per = P.swiglu ? TM / 2 : TM;   // outputs: in all, of a tile
 
   if (threadIdx.x == 0) {
@@ -199,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int slot = 0, issued = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int tile = blockIdx.x; tile < ntiles && ok; tile += gridDim.x) {
+      for (int tile = tile0; tile < ntiles && ok; tile += tiles_step) {
         const int m = tile / Q.tt * per, t = tile % Q.tt * NT;
         for (int s = 0; s < nst; ++s) {
           if (!wait_on(&empty[slot], phase ^ 1u, abort_flag, Q.wait_ns)) {
@@ -209,13 +219,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint8_t* at = smem + slot * C::STAGE;
           if (codes) {
             mbar_expect_tx(&full[slot], kCodeBytes);
-            tma_load_2d(at, &tm_w, &full[slot], s * (KS / 2), m, pol);
-            if (P.swiglu) tma_load_2d(at + kCodeBytes / 2, &tm_w, &full[slot], s * (KS / 2), outs + m, pol);
+            tma_load_2d(at, &tm_w, &full[slot], (s0 + s) * (KS / 2), m, pol);
+            if (P.swiglu) tma_load_2d(at + kCodeBytes / 2, &tm_w, &full[slot], (s0 + s) * (KS / 2), outs + m, pol);
           } else {
             mbar_expect_tx(&full[slot], 2 * C::XB);
 #pragma unroll
             for (int a = 0; a < 2; ++a)
-              tma_load_2d(at + kCodeBytes + a * C::XB, &tm_x, &full[slot], s * KS + a * 64, t, pol);
+              tma_load_2d(at + kCodeBytes + a * C::XB, &tm_x, &full[slot], (s0 + s) * KS + a * 64, t, pol);
           }
           ++issued;
           if (++slot == C::S) {
@@ -255,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto wait = [&](uint64_t* bar, uint32_t ph) {
       return __all_sync(kFull, wait_on(bar, ph, abort_flag, Q.wait_ns)) != 0;
     };
-    for (int tile = blockIdx.x; tile < ntiles && ok; tile += gridDim.x, base += nst) {
+    for (int tile = tile0; tile < ntiles && ok; tile += tiles_step, base += nst) {
       const int own0 = (base + set) & 1;
       for (int s = own0; s < nst && ok; s += 2) {
         ok = wait(&full[slot], phase) && wait(&afull[set], aphase);
@@ -329,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(bar);
     };
     if (Q.stall && blockIdx.x == 0) ok = wait(stall, 0);               // testing aid: runs out
-    for (int tile = blockIdx.x; tile < ntiles && ok; tile += gridDim.x, base += nst) {
+    for (int tile = tile0; tile < ntiles && ok; tile += tiles_step, base += nst) {
       const int first = tile / Q.tt * per, tok0 = tile % Q.tt * NT;
       const int wrow = min(first + out_row, outs - 1) + (P.swiglu && lane >= 16 ? outs : 0);
       const size_t sbase = static_cast<size_t>(wrow) * P.groups;
@@ -337,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto fetch_c = [&](int s, uint32_t (&z)[HC], uint32_t (&f)[HC]) {
 #pragma unroll
         for (int i = 0; i < HC; ++i) {
-          const int k = s * KS + half * 64 + i * HK;
+          const int k = (s0 + s) * KS + half * 64 + i * HK;
           z[i] = 8u;
           f[i] = 0;
           if (k >= P.K) continue;
@@ -352,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto fetch_s = [&](int s, uint32_t (&f)[C::GPS]) {
 #pragma unroll
         for (int j = 0; j < C::GPS; ++j) {
-          const int gi = s * C::GPS + j;
+          const int gi = (s0 + s) * C::GPS + j;
           f[j] = 0;
           if (!C::POST || gi >= P.groups) continue;
           if (FMT == MOE_W_MXFP4) f[j] = 0x10000u | __ldg(static_cast<const uint8_t*>(P.scales) + sbase + gi);
@@ -492,23 +502,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok && (nst > 1 || (base & 1) == 1)) ok = take(1, sc);
       }
       if (!ok) break;
-      // y[t][n]: lanes hold consecutive n
+      // y[t][n] of tokens i and i + 1 of this thread: lanes hold consecutive n
       const int n = first + out_row;
-      if (P.swiglu) {
-        // lanes 0-15 hold h and 16-31 u of the same outputs: each half takes every other token
-#pragma unroll
-        for (int i = 0; i < CN; i += 2) {
-          const float got = __shfl_xor_sync(kFull, lane < 16 ? acc[i + 1] : acc[i], 16);
-          const float h = lane < 16 ? acc[i] : got, u = lane < 16 ? got : acc[i + 1];
-          const int t = tok0 + quarter * CN + i + (lane >> 4);
-          if (n < outs && t < P.T) w4::store_y<BF16>(P, t, n, h / (1.f + expf(-h)) * u);
+      auto store_pair = [&](int i, float v0, float v1) {
+        const int t = tok0 + quarter * CN + i;
+        if (P.swiglu) {
+          // lanes 0-15 hold h and 16-31 u of the same outputs: each half takes one token
+          const float got = __shfl_xor_sync(kFull, lane < 16 ? v1 : v0, 16);
+          const float h = lane < 16 ? v0 : got, u = lane < 16 ? got : v1;
+          if (n < outs && t + (lane >> 4) < P.T) w4::store_y<BF16>(P, t + (lane >> 4), n, h / (1.f + expf(-h)) * u);
+        } else {
+          if (n < outs && t < P.T) w4::store_y<BF16>(P, t, n, v0);
+          if (n < outs && t + 1 < P.T) w4::store_y<BF16>(P, t + 1, n, v1);
         }
-      } else {
+      };
+      if (ck == 1) {
 #pragma unroll
-        for (int i = 0; i < CN; ++i) {
-          const int t = tok0 + quarter * CN + i;
-          if (n < outs && t < P.T) w4::store_y<BF16>(P, t, n, acc[i]);
+        for (int i = 0; i < CN; i += 2) store_pair(i, acc[i], acc[i + 1]);
+        continue;
+      }
+      // A shared tile: every CTA lays its sums out (the stages' memory is free, every
+      // MMA has finished), and each adds up a part of the tokens.
+      float* const red = reinterpret_cast<float*>(smem) + threadIdx.x;
+#pragma unroll
+      for (int i = 0; i < CN; ++i) red[i * kWorkers * 32] = acc[i];
+      cluster_sync();
+      ++meetings;
+      const int share = CN >> Q.ck_bits < 2 ? 2 : CN >> Q.ck_bits;
+      for (int i = rank * share; i < CN && i < (rank + 1) * share; i += 2) {
+        float v0 = 0.f, v1 = 0.f;
+        for (int r = 0; r < ck; ++r) {
+          const uint32_t at = cluster_addr(red + i * kWorkers * 32, r);
+          float a, b;
+          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(a) : "r"(at));
+          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(b) : "r"(at + kWorkers * 128));
+          v0 += a;
+          v1 += b;
         }
+        store_pair(i, v0, v1);
       }
     }
     if (!ok) {
@@ -517,6 +548,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   __syncwarp();
+  if (ck > 1)
+    for (; meetings < 2; ++meetings) cluster_sync();                   // nobody leaves while its memory is read
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -552,9 +585,26 @@ cudaError_t launch(const LinearParams& P, const DeviceInfo& dev, int32_t* status
       encode_tiled_sw128(&tm_x, BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, P.x, xd,
                          xs, xb) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
-  const int64_t tiles = static_cast<int64_t>(Q.mt) * Q.tt, most = dev.sm_count;
-  const cudaError_t e = launch_pdl(kern, dim3(static_cast<unsigned>(tiles < most ? tiles : most)), dim3(kThreads),
-                                   C::SMEM, s, tm_w, tm_x, Q);
+  const int64_t tiles = static_cast<int64_t>(Q.mt) * Q.tt;
+  // Tiles for less than half the SMs: clusters share them, as long as a CTA keeps
+  // four stages.
+  const int nst = (P.K + KS - 1) / KS;
+  while (Q.ck_bits < 3 && tiles << (Q.ck_bits + 1) <= dev.sm_count && nst >> (Q.ck_bits + 1) >= 4) ++Q.ck_bits;
+  const int64_t ctas = Q.ck_bits > 0 ? tiles << Q.ck_bits : tiles < dev.sm_count ? tiles : dev.sm_count;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = 1u << Q.ck_bits;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = Q.ck_bits > 0 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tm_w, tm_x, Q);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -150,10 +150,11 @@ def test_router_grad_parts_and_refusals(moe):
                                                dloss=dloss)).all()
 
 
-@pytest.mark.parametrize("T", [24, 300])
-def test_wait_expiry_of_the_linear_is_reported(moe, T):
+@pytest.mark.parametrize("T", [8, 24, 300])
+def test_wait_expiry_of_the_linear_is_reported(moe, monkeypatch, T):
     """With the testing aids on, CTA 0's workers wait on a barrier nothing arrives
     on: the call reports MOE_ERR_TIMEOUT, and the next one is right again."""
+    monkeypatch.setenv("MOE_LINEAR", "tc")
     w, x = make("int4", 128, 256, 2048, T, zeros=True, seed=13)
     d, xs = cuda(w), x.cuda()
     out, st = torch.empty((T, 256), device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
