@@ -143,7 +143,9 @@ __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile
   return mbar_wait<false>(bar, parity, abort_flag, limit_ns);
 }
 
-template <int FMT, int GROUP, bool BF16, int NT>
+// SHARED: a cluster of CTAs shares a tile's K.  (Its own instance: the few more
+// instructions made the loops of the other one 12 % slower.)
+template <int FMT, int GROUP, bool BF16, int NT, bool SHARED>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
                         const __grid_constant__ TcParams Q) {
@@ -164,9 +166,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // this CTA's stages of K: nst of them from s0 on (all, but for a shared tile)
-  const int ck = 1 << Q.ck_bits, rank = Q.ck_bits == 0 ? 0 : static_cast<int>(cluster_rank());
-  const int all = (P.K + KS - 1) / KS, s0 = all * rank >> Q.ck_bits, nst = (all * (rank + 1) >> Q.ck_bits) - s0;
-  const int ntiles = Q.mt * Q.tt, tile0 = blockIdx.x >> Q.ck_bits, tiles_step = gridDim.x >> Q.ck_bits;
+  const int ck_bits = SHARED ? Q.ck_bits : 0, ck = 1 << ck_bits;
+  const int rank = SHARED ? static_cast<int>(cluster_rank()) : 0;
+  const int all = (P.K + KS - 1) / KS, s0 = all * rank >> ck_bits, nst = (all * (rank + 1) >> ck_bits) - s0;
+  const int ntiles = Q.mt * Q.tt, tile0 = blockIdx.x >> ck_bits, tiles_step = gridDim.x >> ck_bits;
   int meetings = 0;                           // barriers over the cluster: two, on every path
   const int outs = P.swiglu ? P.N >> 1 : P.N, per = P.swiglu ? TM / 2 : TM;   // outputs: in all, of a tile
 
@@ -516,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (n < outs && t + 1 < P.T) w4::store_y<BF16>(P, t + 1, n, v1);
         }
       };
-      if (ck == 1) {
+      if (!SHARED) {
 #pragma unroll
         for (int i = 0; i < CN; i += 2) store_pair(i, acc[i], acc[i + 1]);
         continue;
@@ -528,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < CN; ++i) red[i * kWorkers * 32] = acc[i];
       cluster_sync();
       ++meetings;
-      const int share = CN >> Q.ck_bits < 2 ? 2 : CN >> Q.ck_bits;
+      const int share = CN >> ck_bits < 2 ? 2 : CN >> ck_bits;
       for (int i = rank * share; i < CN && i < (rank + 1) * share; i += 2) {
         float v0 = 0.f, v1 = 0.f;
         for (int r = 0; r < ck; ++r) {
@@ -548,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   __syncwarp();
-  if (ck > 1)
+  if (SHARED)
     for (; meetings < 2; ++meetings) cluster_sync();                   // nobody leaves while its memory is read
   tc_fence_before();
   __syncthreads();
@@ -557,16 +560,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512));
 }
 
-template <int FMT, int GROUP, bool BF16, int NT>
-cudaError_t launch(const LinearParams& P, const DeviceInfo& dev, int32_t* status, cudaStream_t s) {
+template <int FMT, int GROUP, bool BF16, int NT, bool SHARED>
+cudaError_t launch_tiles(const TcParams& Q, const CUtensorMap& tm_w, const CUtensorMap& tm_x, unsigned ctas,
+                         const DeviceInfo& dev, cudaStream_t s) {
   using C = Cfg<FMT, GROUP, BF16, NT>;
-  auto kern = linear_w4_tc_kernel<FMT, GROUP, BF16, NT>;
+  auto kern = linear_w4_tc_kernel<FMT, GROUP, BF16, NT, SHARED>;
   static bool done[64] = {};
   if (!done[dev.id]) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     done[dev.id] = true;
   }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = 1u << Q.ck_bits;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = SHARED ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tm_w, tm_x, Q);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int FMT, int GROUP, bool BF16, int NT>
+cudaError_t launch(const LinearParams& P, const DeviceInfo& dev, int32_t* status, cudaStream_t s) {
   TcParams Q{};
   Q.L = P;
   Q.wait_ns = wait_limit_ns();
@@ -590,22 +613,10 @@ cudaError_t launch(const LinearParams& P, const DeviceInfo& dev, int32_t* status
   // four stages.
   const int nst = (P.K + KS - 1) / KS;
   while (Q.ck_bits < 3 && tiles << (Q.ck_bits + 1) <= dev.sm_count && nst >> (Q.ck_bits + 1) >= 4) ++Q.ck_bits;
-  const int64_t ctas = Q.ck_bits > 0 ? tiles << Q.ck_bits : tiles < dev.sm_count ? tiles : dev.sm_count;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = C::SMEM;
-  cfg.stream = s;
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = 1u << Q.ck_bits;
-  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = Q.ck_bits > 0 ? 2 : 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tm_w, tm_x, Q);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  if (Q.ck_bits > 0)
+    return launch_tiles<FMT, GROUP, BF16, NT, true>(Q, tm_w, tm_x, static_cast<unsigned>(tiles << Q.ck_bits), dev, s);
+  return launch_tiles<FMT, GROUP, BF16, NT, false>(
+      Q, tm_w, tm_x, static_cast<unsigned>(tiles < dev.sm_count ? tiles : dev.sm_count), dev, s);
 }
 
 template <int FMT, int GROUP, bool BF16>
