@@ -426,7 +426,9 @@ __global__ void __launch_bounds__(kThreads, 2) linear_w4_kernel(const __grid_con
         a[i / 2][i % 2][2] = pair_of<FMT, BF16, 2>(w, c[i]);
         a[i / 2][i % 2][3] = pair_of<FMT, BF16, 3>(w, c[i]);
       }
-      constexpr bool POST = FMT != MOE_W_NVFP4;                      // the scale multiplies the group's sum
+      // INT4, MXFP4: the scale multiplies the group's sum.  NVFP4: the stage's sum is
+      // added, so that no run of the tensor cores' truncating additions gets long.
+      constexpr int RUN = FMT == MOE_W_NVFP4 ? KB : GB;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const uint4 v = lds<uint4>(smem, xa[nt] + b * 64);
@@ -439,15 +441,16 @@ __global__ void __launch_bounds__(kThreads, 2) linear_w4_kernel(const __grid_con
         }
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
-          float (&d)[4] = POST ? part[rt][nt] : acc[rt][nt];
-          if (POST && b % GB == 0)
+          float (&d)[4] = part[rt][nt];
+          if (b % RUN == 0)
             mma16816<BF16, true>(d, a[rt][0][0], a[rt][1][0], a[rt][0][1], a[rt][1][1], x0, x1);
           else
             mma16816<BF16, false>(d, a[rt][0][0], a[rt][1][0], a[rt][0][1], a[rt][1][1], x0, x1);
           mma16816<BF16, false>(d, a[rt][0][2], a[rt][1][2], a[rt][0][3], a[rt][1][3], x2, x3);
-          if (POST && (b + 1) % GB == 0) {
+          if ((b + 1) % RUN == 0) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[rt][nt][i] = fmaf(d[i], f[2 * rt + i / 2], acc[rt][nt][i]);
+            for (int i = 0; i < 4; ++i)
+              acc[rt][nt][i] = FMT == MOE_W_NVFP4 ? acc[rt][nt][i] + d[i] : fmaf(d[i], f[2 * rt + i / 2], acc[rt][nt][i]);
           }
         }
       }

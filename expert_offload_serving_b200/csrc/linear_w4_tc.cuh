@@ -60,6 +60,12 @@ struct TcParams {
   uint64_t wait_ns;
   int stall, mt, tt;                          // tiles of rows, of tokens
   int ck_bits;                                // CTAs of a cluster that share a tile's K (log2)
+  // PRE: stages whose products run through one accumulator (log2).  The tensor cores
+  // cut sums off instead of rounding them: 1e-6 of the result per 128 additions,
+  // 1024 of K in two planes.  For an fp32 y the sums are added in registers after 8
+  // stages (4e-7; 7 % of the time at NT = 64, 20 % at 128, whose sets have a single
+  // accumulator), a 16-bit y does not notice and they run on.
+  int run_bits;
   int32_t* status;
 };
 
@@ -143,9 +149,11 @@ __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile
   return mbar_wait<false>(bar, parity, abort_flag, limit_ns);
 }
 
-// SHARED: a cluster of CTAs shares a tile's K.  (Its own instance: the few more
-// instructions made the loops of the other one 12 % slower.)
-template <int FMT, int GROUP, bool BF16, int NT, bool SHARED>
+// SHARED: a cluster of CTAs shares a tile's K.  RUNS: PRE sums are added in registers
+// after each run.  (Instances of their own: the few more instructions of SHARED made
+// the loops of the other one 12 % slower at NT = 64, the sums that RUNS holds across
+// them 14 % at NT = 128.)
+template <int FMT, int GROUP, bool BF16, int NT, bool SHARED, bool RUNS>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
                         const __grid_constant__ TcParams Q) {
@@ -170,6 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int rank = SHARED ? static_cast<int>(cluster_rank()) : 0;
   const int all = (P.K + KS - 1) / KS, s0 = all * rank >> ck_bits, nst = (all * (rank + 1) >> ck_bits) - s0;
   const int ntiles = Q.mt * Q.tt, tile0 = blockIdx.x >> ck_bits, tiles_step = gridDim.x >> ck_bits;
+  const int run = C::POST ? 1 : 1 << (RUNS ? Q.run_bits : 30);
   int meetings = 0;                           // barriers over the cluster: two, on every path
   const int outs = P.swiglu ? P.N >> 1 : P.N, per = P.swiglu ? TM / 2 : TM;   // outputs: in all, of a tile
 
@@ -275,7 +284,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         aphase ^= 1u;
         const uint64_t xd = xdesc + (slot * C::STAGE >> 4);
-        const bool begin = C::POST || s == own0, end = C::POST || s + 2 >= nst;
+        // the set's first and last stage of a run (of one stage, in POST)
+        const bool begin = C::POST || (s & (run - 1)) < 2, end = C::POST || (s & (run - 1)) >= run - 2 || s + 2 >= nst;
 #pragma unroll
         for (int j = 0; j < C::GPS; ++j) {
           if (begin) {
@@ -408,7 +418,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return true;
       };
-      // The groups of stage s; the next stage's scales are on their way meanwhile.
+      // PRE: run r, the accumulators of the sets that have stages in it.
+      const float pre_scale = FMT == MOE_W_NVFP4 ? P.tensor_scale : FMT == MOE_W_MXFP4 ? 4.f : 1.f;
+      auto add_run = [&](int r) {
+        const int n = min(run, nst - r * run);
+        const bool odd = base & 1;                                     // set of the run's first stage (run is even)
+        if ((n > 1 || !odd) && !take(0, pre_scale)) return false;
+        return !(n > 1 || odd) || take(1, pre_scale);
+      };
+      // POST: the groups of stage s; the next stage's scales are on their way meanwhile.
       auto add_up = [&](int s) {
         float f[C::GPS];
 #pragma unroll
@@ -420,12 +438,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!(odd ? take(1, f[j]) : take(0, f[j]))) return false;
         return true;
       };
-      int next = 0;                                                    // the next stage to add up
+      int next = 0;                                                    // the next stage, or run, to add up
       for (int s = own0; s < nst && ok; s += 2) {
         // Stages up to s - 2 are added up before the wait for the buffer that stage
         // s - 2's MMAs read: these may in turn wait for accumulators (a stage can
         // have more groups than there are accumulators).
-        for (; C::POST && next < s - 1 && ok; ++next) ok = add_up(next);
+        for (; (C::POST || RUNS) && next * run + run < s && ok; ++next) ok = C::POST ? add_up(next) : add_run(next);
         uint32_t c[HC], s1[HC], s2[HC];
 #pragma unroll
         for (int i = 0; i < HC; ++i) {
@@ -456,26 +474,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (s + 2 < nst) fetch_c(s + 2, zn, sn);
         const uint32_t w[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
-        uint32_t a[32], lo[C::PLANES == 2 ? 32 : 1];
-        auto expand = [&](auto third) {
+        const uint32_t a_at = tmem + lanes + set * C::AC + half * 32;
+        // four words (16 columns) at a time: registers
+        auto expand = [&](int i0, auto third) {
+          uint32_t a[16], lo[16];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int h = i * 8 / HK;
+          for (int e = 0; e < 4; ++e) {
+            const int i = i0 + e, h = i * 8 / HK;
             const uint32_t up = w[i] >> 4;
-            a[4 * i] = natural_pair<FMT, BF16, 0>(w[i], up, c[h]);
-            a[4 * i + 1] = natural_pair<FMT, BF16, 1>(w[i], up, c[h]);
-            a[4 * i + 2] = natural_pair<FMT, BF16, 2>(w[i], up, c[h]);
-            a[4 * i + 3] = natural_pair<FMT, BF16, 3>(w[i], up, c[h]);
+            a[4 * e] = natural_pair<FMT, BF16, 0>(w[i], up, c[h]);
+            a[4 * e + 1] = natural_pair<FMT, BF16, 1>(w[i], up, c[h]);
+            a[4 * e + 2] = natural_pair<FMT, BF16, 2>(w[i], up, c[h]);
+            a[4 * e + 3] = natural_pair<FMT, BF16, 3>(w[i], up, c[h]);
             if constexpr (!C::POST && FMT == MOE_W_MXFP4) {
 #pragma unroll
-              for (int p = 4 * i; p < 4 * i + 4; ++p) a[p] = w4::mul2<true>(a[p], s1[h]);
+              for (int p = 4 * e; p < 4 * e + 4; ++p) a[p] = w4::mul2<true>(a[p], s1[h]);
             }
             if constexpr (C::PLANES == 2) {
               // (code - zero) * scale = hi + lo: hi rounded, lo what is left, exact.  The
               // first plane holds -hi (the MMA negates it), which lo's one fused
               // multiply-add takes as it is.
 #pragma unroll
-              for (int p = 4 * i; p < 4 * i + 4; ++p) {
+              for (int p = 4 * e; p < 4 * e + 4; ++p) {
                 const uint32_t v = a[p];
                 a[p] = w4::mul2<true>(v, s1[h] ^ 0x80008000u);
                 lo[p] = fma2(v, s1[h], a[p]);
@@ -483,27 +503,27 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
+          if (i0 == 0) {
+            ok = wait(&aempty[set], aphase ^ 1u);
+            tc_fence_after();
+          }
+          tmem_st16(a_at + i0 * 4, a);
+          if constexpr (C::PLANES == 2) tmem_st16(a_at + kACols + i0 * 4, lo);
         };
-        if (C::PLANES == 2 && P.scale_type != MOE_DT_BF16) expand(std::true_type());
-        else expand(std::false_type());
-        if (!wait(&aempty[set], aphase ^ 1u)) {
-          ok = false;
-          break;
+        if (C::PLANES == 2 && P.scale_type != MOE_DT_BF16) {
+          expand(0, std::true_type());
+          expand(4, std::true_type());
+        } else {
+          expand(0, std::false_type());
+          expand(4, std::false_type());
         }
+        tmem_st_wait();
+        if (!ok) break;
         aphase ^= 1u;
-        tc_fence_after();
-        tmem_st32(tmem + lanes + set * C::AC + half * 32, a);
-        if constexpr (C::PLANES == 2) tmem_st32(tmem + lanes + set * C::AC + kACols + half * 32, lo);
         tc_fence_before();
         arrive(&afull[set]);
       }
-      if (C::POST) {
-        for (; next < nst && ok; ++next) ok = add_up(next);
-      } else {                                                         // one accumulator a set, over its stages
-        const float sc = FMT == MOE_W_NVFP4 ? P.tensor_scale : FMT == MOE_W_MXFP4 ? 4.f : 1.f;
-        if (ok && (nst > 1 || (base & 1) == 0)) ok = take(0, sc);
-        if (ok && (nst > 1 || (base & 1) == 1)) ok = take(1, sc);
-      }
+      for (; next * run < nst && ok; ++next) ok = C::POST ? add_up(next) : add_run(next);
       if (!ok) break;
       // y[t][n] of tokens i and i + 1 of this thread: lanes hold consecutive n
       const int n = first + out_row;
@@ -560,11 +580,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512));
 }
 
-template <int FMT, int GROUP, bool BF16, int NT, bool SHARED>
+template <int FMT, int GROUP, bool BF16, int NT, bool SHARED, bool RUNS>
 cudaError_t launch_tiles(const TcParams& Q, const CUtensorMap& tm_w, const CUtensorMap& tm_x, unsigned ctas,
                          const DeviceInfo& dev, cudaStream_t s) {
   using C = Cfg<FMT, GROUP, BF16, NT>;
-  auto kern = linear_w4_tc_kernel<FMT, GROUP, BF16, NT, SHARED>;
+  auto kern = linear_w4_tc_kernel<FMT, GROUP, BF16, NT, SHARED, RUNS>;
   static bool done[64] = {};
   if (!done[dev.id]) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
@@ -595,6 +615,7 @@ cudaError_t launch(const LinearParams& P, const DeviceInfo& dev, int32_t* status
   Q.wait_ns = wait_limit_ns();
   Q.stall = test_stall();
   Q.status = status;
+  Q.run_bits = P.y_f32 ? 3 : 30;
   const int outs = P.swiglu ? P.N / 2 : P.N, per = P.swiglu ? TM / 2 : TM;
   Q.mt = (outs + per - 1) / per;
   Q.tt = (P.T + NT - 1) / NT;
@@ -613,10 +634,16 @@ cudaError_t launch(const LinearParams& P, const DeviceInfo& dev, int32_t* status
   // four stages.
   const int nst = (P.K + KS - 1) / KS;
   while (Q.ck_bits < 3 && tiles << (Q.ck_bits + 1) <= dev.sm_count && nst >> (Q.ck_bits + 1) >= 4) ++Q.ck_bits;
-  if (Q.ck_bits > 0)
-    return launch_tiles<FMT, GROUP, BF16, NT, true>(Q, tm_w, tm_x, static_cast<unsigned>(tiles << Q.ck_bits), dev, s);
-  return launch_tiles<FMT, GROUP, BF16, NT, false>(
-      Q, tm_w, tm_x, static_cast<unsigned>(tiles < dev.sm_count ? tiles : dev.sm_count), dev, s);
+  const unsigned ctas = static_cast<unsigned>(Q.ck_bits > 0            ? tiles << Q.ck_bits
+                                              : tiles < dev.sm_count ? tiles
+                                                                     : dev.sm_count);
+  if constexpr (!Cfg<FMT, GROUP, BF16, NT>::POST && NT == 128) {
+    if (!P.y_f32)
+      return Q.ck_bits > 0 ? launch_tiles<FMT, GROUP, BF16, NT, true, false>(Q, tm_w, tm_x, ctas, dev, s)
+                           : launch_tiles<FMT, GROUP, BF16, NT, false, false>(Q, tm_w, tm_x, ctas, dev, s);
+  }
+  return Q.ck_bits > 0 ? launch_tiles<FMT, GROUP, BF16, NT, true, true>(Q, tm_w, tm_x, ctas, dev, s)
+                       : launch_tiles<FMT, GROUP, BF16, NT, false, true>(Q, tm_w, tm_x, ctas, dev, s);
 }
 
 template <int FMT, int GROUP, bool BF16>

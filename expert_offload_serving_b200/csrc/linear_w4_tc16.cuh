@@ -1,5 +1,5 @@
 // The dense 4-bit linear on the 5th-generation tensor cores for up to 16 tokens
-// and many rows.
+// and many rows, INT4 (groups of 64 or 128) and MXFP4.
 //
 // As linear_w4_tc.cuh, cut for a narrow product.  With 16 columns the MMAs take
 // next to no time, and what counts is instructions per weight and hand-overs per
@@ -36,8 +36,8 @@ constexpr int kXAtom = NT * 128;              // 64 elements of the token rows
 
 template <int FMT, int GROUP>
 struct Cfg {
-  static constexpr bool POST = FMT != MOE_W_NVFP4;
-  static constexpr int GPS = POST ? KS / GROUP : 1;                    // groups of a stage: 2, 4, 8
+  static_assert(FMT == MOE_W_INT4 || FMT == MOE_W_MXFP4, "scales of groups");
+  static constexpr int GPS = KS / GROUP;                               // groups of a stage: 2, 4, 8
   static constexpr int DCOLS = GPS * NT;                               // TMEM columns of its accumulators
   static constexpr int ND = (512 - 2 * kACols) / 2 / DCOLS < 2 ? 1 : 2;   // ... that a set has
   static constexpr int TOKENS = GPS == 2 ? 8 : 16;                     // tokens a thread adds up
@@ -174,8 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int tile = blockIdx.x; tile < Q.mt && ok; tile += gridDim.x, base += nst) {
       const int own0 = (base + set) & 1;
       for (int s = own0; s < nst; s += 2) {
-        const bool begin = C::POST || s == own0, end = C::POST || s + 2 >= nst;
-        ok = wait(&full[slot], phase) && wait(&afull[set], aphase) && (!begin || wait(&de[d], dphase ^ 1u));
+        ok = wait(&full[slot], phase) && wait(&afull[set], aphase) && wait(&de[d], dphase ^ 1u);
         if (!ok) break;
         aphase ^= 1u;
         tc_fence_after();
@@ -186,14 +185,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr int MMAS = KS / 16 / C::GPS;                     // of a group
             tc_mma_f16_ts(d_set + d * C::DCOLS + kk / MMAS * NT, a_tmem + kk * 8,
                           xd + (((kk >> 2) * kXAtom) >> 4) + 2 * (kk & 3), idesc,
-                          kk % MMAS > 0 || !begin ? 1u : 0u);
+                          kk % MMAS > 0 ? 1u : 0u);
           }
-          if (end) tc_commit(&df[d]);
+          tc_commit(&df[d]);
           tc_commit(&aempty[set]);
           tc_commit(&empty[slot]);
         }
         __syncwarp();
-        if (end && ++d == C::ND) {
+        if (++d == C::ND) {
           d = 0;
           dphase ^= 1u;
         }
@@ -217,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int lrow = quad * 32 + lane;                                 // TMEM lane
     const int out_row = P.swiglu ? quad * 16 + (lane & 15) : lrow;     // output of the tile
     const int srow = P.swiglu && lane >= 16 ? TM / 2 + out_row : out_row;   // row of the stage
-    constexpr int HC = FMT == MOE_W_NVFP4 ? 8 : 128 / GROUP;           // groups of half a stage
+    constexpr int HC = 128 / GROUP;                                    // groups of half a stage
     constexpr int HK = 128 / HC;
     // first of this thread's groups of a stage (then every fourth) and of its tokens
     const int my_group = C::GPS == 2 ? quarter >> 1 : quarter;
@@ -237,25 +236,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int first = tile * per;
       const int wrow = min(first + out_row, outs - 1) + (P.swiglu && lane >= 16 ? outs : 0);
       const size_t sbase = static_cast<size_t>(wrow) * P.groups;
-      // raw zeros, or NVFP4 scales (0x100 or more: there is one), of a stage's half ...
+      // zeros of a stage's half ...
       auto fetch_c = [&](int s, uint32_t (&z)[HC]) {
 #pragma unroll
         for (int i = 0; i < HC; ++i) {
           const int k = s * KS + half * 128 + i * HK;
-          z[i] = FMT == MOE_W_INT4 ? 8u : 0u;
-          if (k >= P.K) continue;
-          const size_t at = sbase + k / GROUP;
-          if (FMT == MOE_W_INT4 && P.zeros != nullptr) z[i] = __ldg(P.zeros + at) & 15u;
-          if (FMT == MOE_W_NVFP4) z[i] = 0x100u | __ldg(static_cast<const uint8_t*>(P.scales) + at);
+          z[i] = 8u;
+          if (FMT == MOE_W_INT4 && P.zeros != nullptr && k < P.K) z[i] = __ldg(P.zeros + sbase + k / GROUP) & 15u;
         }
       };
-      // ... and the scales of this thread's groups of a stage (POST)
+      // ... and the scales of this thread's groups of a stage
       auto fetch_s = [&](int s, uint32_t (&f)[C::MINE]) {
 #pragma unroll
         for (int j = 0; j < C::MINE; ++j) {
           const int gi = s * C::GPS + my_group + 4 * j;
           f[j] = 0;
-          if (!C::POST || gi >= P.groups) continue;
+          if (gi >= P.groups) continue;
           if (FMT == MOE_W_MXFP4) f[j] = 0x100u | __ldg(static_cast<const uint8_t*>(P.scales) + sbase + gi);
           else if (P.scale_type == MOE_DT_F32) f[j] = __ldg(static_cast<const uint32_t*>(P.scales) + sbase + gi);
           else f[j] = __ldg(static_cast<const uint16_t*>(P.scales) + sbase + gi);
@@ -283,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int j = 0; j < C::MINE; ++j) {
           float v[C::TOKENS];
-          w4tc::tmem_load(tmem_d + lanes + di * C::DCOLS + (C::POST ? (my_group + 4 * j) * NT + my_token : 0), v);
+          w4tc::tmem_load(tmem_d + lanes + di * C::DCOLS + (my_group + 4 * j) * NT + my_token, v);
           const float2 s2 = make_float2(sc[j], sc[j]);
 #pragma unroll
           for (int i = 0; i < C::TOKENS; i += 2) {
@@ -314,11 +310,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int s = own0; s < nst && ok; s += 2) {
         // stages up to s - 2 first: the MMAs of stage s - 2, whose A buffer is next,
         // may wait for accumulators
-        for (; C::POST && next < s - 1 && ok; ++next) ok = add_up(next);
+        for (; next < s - 1 && ok; ++next) ok = add_up(next);
         uint32_t c[HC];
 #pragma unroll
         for (int i = 0; i < HC; ++i)
-          c[i] = FMT == MOE_W_NVFP4 && zn[i] == 0 ? 0u : w4tc::pair_constant<FMT, BF16>(zn[i] & 255u);
+          c[i] = w4tc::pair_constant<FMT, BF16>(zn[i]);
         if (!ok || !wait(&full[slot], phase)) {
           ok = false;
           break;
@@ -361,26 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         arrive(&afull[set]);
       }
-      if (C::POST) {
-        for (; next < nst && ok; ++next) ok = add_up(next);
-      } else if (quarter == 0) {                                       // one accumulator a set, over its stages
-        float sc[C::MINE];
-#pragma unroll
-        for (int j = 0; j < C::MINE; ++j) sc[j] = P.tensor_scale;
-        if (ok && (nst > 1 || (base & 1) == 0)) ok = take(0, sc);
-        if (ok && (nst > 1 || (base & 1) == 1)) ok = take(1, sc);
-      } else {
-        // (the barrier counts every warp)
-        for (int st = 0; st < 2; ++st) {
-          if (nst == 1 && (base & 1) != st) continue;
-          if (ok) ok = wait(&dfull[st * C::ND + d[st]], dphase[st]);
-          arrive(&dempty[st * C::ND + d[st]]);
-          if (++d[st] == C::ND) {
-            d[st] = 0;
-            dphase[st] ^= 1u;
-          }
-        }
-      }
+      for (; next < nst && ok; ++next) ok = add_up(next);
       // the quarters' sums, each thread's row and tokens, through shared memory
       if (!ok || !wait(rempty, rphase ^ 1u)) {
         ok = false;
@@ -404,9 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           y[i] = r[0] + r[2 * TM * (C::TOKENS + 1)];
         } else {
           const float* r = red + lrow * (C::TOKENS + 1) + t;
-          y[i] = r[0];
-          if (C::POST)
-            y[i] += r[TM * (C::TOKENS + 1)] + r[2 * TM * (C::TOKENS + 1)] + r[3 * TM * (C::TOKENS + 1)];
+          y[i] = r[0] + r[TM * (C::TOKENS + 1)] + r[2 * TM * (C::TOKENS + 1)] + r[3 * TM * (C::TOKENS + 1)];
         }
       }
       arrive(rempty);

@@ -5,10 +5,13 @@
 namespace moe {
 namespace {
 
+// Up to 16 tokens the narrow kernel, for the formats that it is the faster one for.
 template <int FMT, int GROUP, bool BF16>
 cudaError_t launch(const LinearParams& P, const DeviceInfo& dev, int32_t* status, cudaStream_t s) {
-  return P.T <= w4t16::NT ? w4t16::launch<FMT, GROUP, BF16>(P, dev, status, s)
-                          : w4tc::launch_tokens<FMT, GROUP, BF16>(P, dev, status, s);
+  if constexpr (FMT == MOE_W_MXFP4 || (FMT == MOE_W_INT4 && GROUP >= 64)) {
+    if (P.T <= w4t16::NT) return w4t16::launch<FMT, GROUP, BF16>(P, dev, status, s);
+  }
+  return w4tc::launch_tokens<FMT, GROUP, BF16>(P, dev, status, s);
 }
 
 }  // namespace
