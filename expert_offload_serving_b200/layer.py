@@ -13,6 +13,7 @@ are, MoeLayer.balance and MoeLayer.router_grad.
 """
 from __future__ import annotations
 
+import contextlib
 import threading
 import time
 
@@ -112,7 +113,8 @@ class SharedExpert:
     then the I up rows; down: the same of [d, I].  fmt "int4" (group 32, 64 or
     128), "mxfp4" or "nvfp4" (tensor_scales = the two fp32 scales).  Two
     launches; the activations between them are rounded to x's type, which the
-    second product takes."""
+    second product takes.  They lie in a buffer of the expert's own: calls of one
+    SharedExpert (in streams or captured graphs) may not overlap."""
 
     def __init__(self, gate_up, down, fmt="int4", group=128, tensor_scales=(1.0, 1.0), T_max=1,
                  dtype=torch.bfloat16):
@@ -128,9 +130,9 @@ class SharedExpert:
         self.a = torch.empty((T_max, self.I), dtype=dtype, device=dev)
         self.status = torch.zeros((1,), dtype=torch.int32, device=dev)
 
-    def add(self, x, out, accumulate=True, stream=None):
+    def add(self, x, out, accumulate=True, dev_status=None, stream=None):
         """out [T, d] (fp32, or x's type) += the expert of x [T, d], or = with
-        accumulate=False."""
+        accumulate=False.  dev_status: the status word to use (None: self.status)."""
         T = x.shape[0]
         if T > self.a.shape[0] or x.dtype != self.a.dtype:
             raise ValueError(f"x {x.dtype} {tuple(x.shape)}: expected {self.a.dtype} and at most {self.a.shape[0]} tokens")
@@ -138,7 +140,7 @@ class SharedExpert:
                 (self.gate_up, self.tensor_scales[0], x, self.a[:T], True, False),
                 (self.down, self.tensor_scales[1], self.a[:T], out, False, accumulate)):
             moe_linear_w4(src, codes, scales, dst, fmt=self.fmt, group=self.group, zeros=zeros, tensor_scale=ts,
-                          swiglu=swiglu, accumulate=acc, dev_status=self.status, stream=stream)
+                          swiglu=swiglu, accumulate=acc, dev_status=self.status if dev_status is None else dev_status, stream=stream)
         return out
 
 
@@ -150,7 +152,8 @@ class MoeLayer:
     managed by the LRU cache -- or `cache` (an ExpertCache shared by several
     layers) and this layer's `layer_id` in it; call `prepare(step, experts)`
     to fill.  act="nvfp4" selects the FP4 tensor-core FFN (fused combine).
-    shared (a SharedExpert with bf16 activations): forward() adds its output."""
+    shared (a SharedExpert with bf16 activations): forward() and split_step()
+    add its output; it reports to the layer's status word."""
 
     def __init__(self, E, d, I, fmt, k, T_max, device="cuda", device_pool=None, host_pool=None,
                  n_slots=None, act="none", cache=None, layer_id=0, shared=None):
@@ -356,7 +359,9 @@ class MoeLayer:
                 raise err[0]
             with torch.cuda.stream(s):
                 b["hp_dev"][:T].copy_(b["hp"][:T], non_blocking=True)
-        self.combine(T, host_partial=b["hp_dev"][:T] if host else None, stream=s)
+        if self.shared is not None:
+            self.shared.add(x, b["hp_dev"][:T], accumulate=bool(host), dev_status=self.status, stream=s)
+        self.combine(T, host_partial=b["hp_dev"][:T] if host or self.shared is not None else None, stream=s)
         return dict(hits=hits, filled=filled, host=host, fills=fills, host_ms=host_ms[0])
 
     def forward(self, logits, x, host_partial=None, stream=None):
@@ -386,7 +391,7 @@ class MoeLayer:
             if host_partial is not None:
                 with torch.cuda.stream(torch.cuda.ExternalStream(s) if isinstance(s, int) else s):
                     so.copy_(host_partial)
-            self.shared.add(x, so, accumulate=host_partial is not None, stream=s)
+            self.shared.add(x, so, accumulate=host_partial is not None, dev_status=self.status, stream=s)
             host_partial = so
         s = s if isinstance(s, int) else s.cuda_stream
         hp = 0 if host_partial is None else host_partial.data_ptr()
@@ -400,50 +405,53 @@ class MoeLayer:
     def balance(self, logits, seq_offsets=None, mask=None, stream=None):
         """The balance loss and statistics of the routing the last forward() (or
         route()) of these logits left in idx: dict(loss [2], counts [S, E], prob
-        [S, E], coef [S + 1]), new tensors."""
+        [S, E], coef [S + 1]), new tensors (of `stream`, if it is given)."""
         T = self._check_T(logits.shape[0])
         S = 1 if seq_offsets is None else seq_offsets.numel() - 1
         f32 = dict(dtype=torch.float32, device=self.dev)
-        r = dict(loss=torch.empty((2,), **f32), counts=torch.empty((S, self.E), dtype=torch.int32, device=self.dev),
-                 prob=torch.empty((S, self.E), **f32), coef=torch.empty((S + 1,), **f32))
-        ws = torch.empty((max(1, moe_balance_loss_workspace_bytes(T, self.E, S)),), dtype=torch.uint8, device=self.dev)
+        with self._memory_of(stream):
+            r = dict(loss=torch.empty((2,), **f32), counts=torch.empty((S, self.E), dtype=torch.int32, device=self.dev),
+                     prob=torch.empty((S, self.E), **f32), coef=torch.empty((S + 1,), **f32))
+            ws = torch.empty((max(1, moe_balance_loss_workspace_bytes(T, self.E, S)),), dtype=torch.uint8,
+                             device=self.dev)
         moe_balance_loss(logits, self.idx[:T], r["loss"], r["counts"], r["prob"], r["coef"], ws,
                          seq_offsets=seq_offsets, mask=mask, dev_status=self.status, stream=stream)
-        self._keep(stream, ws, *r.values())
         return r
 
     def router_grad(self, logits, dout=None, balance=None, dloss=None, seq_offsets=None, mask=None, stream=None):
         """d(loss)/d(logits) [T, E], the experts held fixed: of the layer's output
         (dout [T, d], the gradient at forward()'s result; needs y_perm of the last
         forward, so not act="nvfp4") and of the balance losses (balance: the dict
-        of balance(); dloss [2]: their weights).  Either part may be left out."""
+        of balance(); dloss [2]: their weights).  Either part may be left out.  A new
+        tensor (of `stream`, if it is given)."""
         T = self._check_T(logits.shape[0])
         dgate = None
         if dout is not None:
             if self.y_perm is None:
                 raise RuntimeError("act='nvfp4' keeps no expert outputs: the gates have no gradient there")
             self._check_tensor("dout", dout, (T, self.d), torch.float32)
-            dgate = torch.empty((T, self.k), dtype=torch.float32, device=self.dev)
+            with self._memory_of(stream):
+                dgate = torch.empty((T, self.k), dtype=torch.float32, device=self.dev)
             moe_combine_backward(self.y_perm, self.idx[:T], self.gate[:T], self.inv_perm, self.slot, dout, self.E, dgate,
                                  stream=stream)
             self._record_reads_done(stream)              # it reads the slot table, as combine does
         if (dloss is None) != (balance is None):
             raise ValueError("dloss and balance go together")
         b = balance or {}
-        dlogits = torch.empty((T, self.E), dtype=torch.float32, device=self.dev)
+        with self._memory_of(stream):
+            dlogits = torch.empty((T, self.E), dtype=torch.float32, device=self.dev)
         moe_router_backward(logits, self.idx[:T], dlogits, gate=self.gate[:T] if dgate is not None else None,
                             dgate=dgate, counts=b.get("counts"), coef=b.get("coef"), dloss=dloss,
                             seq_offsets=seq_offsets, mask=mask, dev_status=self.status, stream=stream)
-        self._keep(stream, dlogits, *([] if dgate is None else [dgate]))
         return dlogits
 
-    def _keep(self, stream, *tensors):
-        """Tensors allocated here and used on a stream of the caller's: their
-        memory is not reused before that stream has passed."""
-        if stream is not None:
-            s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
-            for t in tensors:
-                t.record_stream(s)
+    @staticmethod
+    def _memory_of(stream):
+        """Tensors made within come from the memory of the caller's stream, where they
+        are used: a block of the current stream's may still have its last use to come."""
+        if stream is None:
+            return contextlib.nullcontext()
+        return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
 
 
 class StreamedPrefill:

@@ -188,3 +188,109 @@ def test_both_kernels_at_every_token_count(moe, monkeypatch, path, fmt, group):
             out = torch.empty((T, 200), dtype=DT["f32"], device="cuda")
             call(moe, cuda(w), xs.cuda(), out)
             check(out, w, xs, "f32")
+
+
+def test_results_on_a_stream_take_no_memory_that_another_still_uses(moe):
+    """balance() and router_grad() with a stream of their own: their tensors come
+    from that stream, not from a block that the current one has yet to write."""
+    T, E = 4096, 256
+    from expert_offload_serving_b200.layer import MoeLayer
+    layer = MoeLayer(E, 512, 256, "bf16", 4, T, device_pool=torch.zeros(
+        (1, moe.moe_expert_blob_bytes(moe.shape(E, 512, 256, "bf16"))), dtype=torch.uint8, device="cuda"))
+    logits = torch.randn((T, E), device="cuda", generator=torch.Generator("cuda").manual_seed(7))
+    layer.route(logits)
+    dloss = torch.ones(2, device="cuda")
+    want = layer.router_grad(logits, balance=layer.balance(logits), dloss=dloss).clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    bal = layer.balance(logits, stream=side)
+    torch.cuda.synchronize()
+    junk = [torch.empty((T, E), device="cuda") for _ in range(4)]
+    torch.cuda._sleep(200_000_000)                     # ~0.1 s: the fills are pending while the gradient is formed
+    for j in junk:
+        j.fill_(float("nan"))
+    del junk, j
+    got = layer.router_grad(logits, balance=bal, dloss=dloss, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("q", [0.0, 0.5])
+def test_split_step_adds_the_shared_expert(moe, q):
+    """A cached layer's split step: routed experts (filled, or computed by the host)
+    + shared expert."""
+    from expert_offload_serving_b200.layer import MoeLayer, pack_pool
+    cfg = synth.LayerConfig("shared_split", E=16, k=4, d=512, I=256, fmt="mxfp4", bias_std=0.5, n_slots=12)
+    w = synth.make_experts(cfg, range(16), 8, device="cpu")
+    sh, wgu, wd = shared_expert("int4", 128, 512, 256, 3, seed=9)
+    layer = MoeLayer(16, 512, 256, "mxfp4", 4, 3, host_pool=pack_pool(16, 512, 256, "mxfp4", w, range(16)), n_slots=12,
+                     shared=sh)
+    for t in range(2):
+        logits, x = synth.make_routing(cfg, 3, 20 + t)
+        layer.split_step(t, logits.cuda(), x.cuda(), q=q, threads=2)
+        ref = M.moe_layer(x.double().numpy(), logits.numpy(), 4, lambda e: M.dequant_expert("mxfp4", w, e))["out"]
+        a = torch.from_numpy(O.linear(x.double().numpy(), wgu, swiglu=True)).to(torch.bfloat16).double().numpy()
+        out = layer.out[:3].cpu().numpy()
+        check_tol(out, ref + O.linear(a, wd))
+        # the routed part, 1e-3 of the sum: what is left of it after fp32 rounding (1e-7 of the sum) is good to 1e-3
+        alone = sh.add(x.cuda(), torch.empty((3, 512), device="cuda"), accumulate=False)
+        check_tol(out.astype(np.float64) - alone.double().cpu().numpy(), ref)
+        moe.moe_check_status(layer.status)
+
+
+def test_a_timeout_of_the_shared_expert_reaches_the_layer(moe, monkeypatch):
+    monkeypatch.setenv("MOE_LINEAR", "tc")
+    cfg = synth.LayerConfig("shared", E=8, k=2, d=512, I=256, fmt="bf16")
+    b = Built(cfg, 4, seed=3)
+    sh, _, _ = shared_expert("int4", 128, 512, 256, 4)
+    from expert_offload_serving_b200.layer import MoeLayer
+    layer = MoeLayer(8, 512, 256, "bf16", 2, 4, device_pool=b.layer.pool, shared=sh)
+    layer.slot.copy_(b.layer.slot)
+    prev = moe.moe_set_wait_limit_ns(5_000_000)
+    moe.moe_set_test_stall(True)
+    try:
+        sh.add(b.x.cuda(), torch.zeros((4, 512), device="cuda"), dev_status=layer.status)
+        with pytest.raises(moe.MoeError) as e:
+            moe.moe_check_status(layer.status)
+        assert e.value.status == moe.MOE_ERR_TIMEOUT
+    finally:
+        moe.moe_set_test_stall(False)
+        moe.moe_set_wait_limit_ns(prev)
+    layer.forward(b.logits.cuda(), b.x.cuda())
+    moe.moe_check_status(layer.status)
+
+
+def test_captured_step_with_shared_expert_and_router_gradient(moe):
+    """forward, balance and router_grad in one graph while an eager pass of the same
+    layer lives: replays of new inputs agree with eager passes."""
+    cfg = synth.LayerConfig("graph", E=8, k=2, d=512, I=256, fmt="bf16")
+    T = 20
+    b = Built(cfg, T, seed=11, experts=range(8))
+    sh, _, _ = shared_expert("mxfp4", 32, 512, 192, T, seed=3)
+    from expert_offload_serving_b200.layer import MoeLayer
+    layer = MoeLayer(8, 512, 256, "bf16", 2, T, device_pool=b.layer.pool, shared=sh)
+    layer.slot.copy_(b.layer.slot)
+    logits, x = b.logits.cuda(), b.x.cuda()
+    dout, dloss = torch.randn((T, 512), device="cuda"), torch.tensor([0.3, 0.2], device="cuda")
+
+    def step():
+        out = layer.forward(logits, x)
+        bal = layer.balance(logits)
+        return out, bal["loss"], layer.router_grad(logits, dout, bal, dloss)
+    eager = step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        captured = step()
+    for seed in (1, 2):
+        l2, x2 = synth.make_routing(cfg, T, 40 + seed)
+        logits.copy_(l2)
+        x.copy_(x2)
+        want = [t.clone() for t in step()]
+        for t in captured:
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        for a, c in zip(want, captured):
+            assert torch.equal(a, c)
+    del eager
