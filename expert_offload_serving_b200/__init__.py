@@ -290,7 +290,8 @@ def moe_layer_forward(s: moe_shape, logits, x, k: int, idx, gate, offsets, perm,
 
 
 # The calls below are short kernels, so the host's share of a call counts: their
-# tensors are checked and handed to the library in C++ (native.cpp).
+# tensors are checked and handed to the library in C++ (native.cpp).  What a call
+# writes may overlap nothing else that it is given (ValueError).
 _nat = None
 
 

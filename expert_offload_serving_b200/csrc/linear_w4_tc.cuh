@@ -61,10 +61,11 @@ struct TcParams {
   int stall, mt, tt;                          // tiles of rows, of tokens
   int ck_bits;                                // CTAs of a cluster that share a tile's K (log2)
   // PRE: stages whose products run through one accumulator (log2).  The tensor cores
-  // cut sums off instead of rounding them: 1e-6 of the result per 128 additions,
-  // 1024 of K in two planes.  For an fp32 y the sums are added in registers after 8
-  // stages (4e-7; 7 % of the time at NT = 64, 20 % at 128, whose sets have a single
-  // accumulator), a 16-bit y does not notice and they run on.
+  // cut sums off instead of rounding them: K = 16384 in two planes through one
+  // accumulator is off by 2.4e-6 of the result's norm.  For an fp32 y the sums are
+  // added in registers after 8 stages (4.8e-7; 7 % of the time at NT = 64, 20 % at
+  // 128, whose sets have a single accumulator), a 16-bit y does not notice and they
+  // run on.
   int run_bits;
   int32_t* status;
 };

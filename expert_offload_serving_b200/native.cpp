@@ -119,6 +119,30 @@ int fits_int(const char* name, int64_t v) {
   return static_cast<int>(v);
 }
 
+// The memory of a call's tensors: what it writes overlaps nothing else of it.
+class Memory {
+ public:
+  void in(const char* name, const void* p, int64_t bytes) { add({name, reinterpret_cast<uintptr_t>(p), bytes, false}); }
+  void out(const char* name, const void* p, int64_t bytes) { add({name, reinterpret_cast<uintptr_t>(p), bytes, true}); }
+
+ private:
+  struct Range {
+    const char* name;
+    uintptr_t at;
+    int64_t bytes;
+    bool written;
+  };
+  void add(const Range& r) {
+    if (r.at == 0 || r.bytes <= 0) return;
+    for (int i = 0; i < n_; ++i)
+      if ((r.written || r_[i].written) && r.at < r_[i].at + r_[i].bytes && r_[i].at < r.at + r.bytes)
+        refuse(std::string(r.name) + " overlaps " + r_[i].name);
+    r_[n_++] = r;
+  }
+  Range r_[16];
+  int n_ = 0;
+};
+
 // Runs a call with its arguments counted and C++ exceptions turned into Python's.
 template <typename F>
 PyObject* guarded(const char* name, Py_ssize_t n, Py_ssize_t want, F f) {
@@ -172,6 +196,17 @@ PyObject* linear_w4(PyObject*, PyObject* const* a, Py_ssize_t n) {
     int32_t* status = static_cast<int32_t*>(mem("dev_status", tensor("dev_status", a[9], true), 1, at::kInt, dev));
     const cudaStream_t stream = stream_of(a[10], dev);
     const int t = fits_int("T", T);
+    // x and out may be columns of one buffer, the same distance between their rows
+    const int64_t xe = x.element_size(), ye = out.element_size(), yw = out.size(1) * ye, pitch = ldx * xe;
+    const int64_t xb = T > 0 ? (T - 1) * pitch + K * xe : 0, yb = T > 0 ? (T - 1) * ldy * ye + yw : 0;
+    const int64_t gap = static_cast<char*>(out.data_ptr()) - static_cast<char*>(x.data_ptr());
+    const int64_t col = T > 1 && pitch > 0 && pitch == ldy * ye ? (gap % pitch + pitch) % pitch : -1;
+    Memory m;
+    m.out("out", out.data_ptr(), yb);
+    if (!(col >= K * xe && col + yw <= pitch)) m.in("x", x.data_ptr(), xb);
+    m.in("codes", pc, codes.numel());
+    m.in("scales", ps, scales.numel() * scales.element_size());
+    if (zeros != nullptr) m.in("zeros", pz, zeros->numel());
     MOE_CALL(r, moe_linear_w4(s, pc, ps, static_cast<const uint8_t*>(pz), static_cast<float>(ts), x.data_ptr(), xt, ldx,
                               t, out.data_ptr(), yt, ldy, flags, status, stream))
     return r;
@@ -211,6 +246,12 @@ struct Batch {
   int32_t* i32(const char* name, PyObject* o, int64_t n, bool optional = false) const {
     return static_cast<int32_t*>(mem(name, tensor(name, o, optional), n, at::kInt, dev));
   }
+  void into(Memory& m) const {
+    m.in("logits", logits, int64_t(T) * E * 4);
+    m.in("idx", idx, int64_t(T) * k * 4);
+    m.in("seq_offsets", off, (int64_t(S) + 1) * 4);
+    m.in("mask", mask, T);
+  }
 };
 
 // (logits, idx, loss, counts, prob, coef, workspace, seq_offsets, mask, dev_status, stream)
@@ -227,6 +268,13 @@ PyObject* balance_loss(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const size_t bytes = static_cast<size_t>(w.numel());
     int32_t* status = b.i32("dev_status", a[9], 1, true);
     const cudaStream_t stream = stream_of(a[10], b.dev);
+    Memory m;
+    b.into(m);
+    m.out("loss", loss, 8);
+    m.out("counts", counts, SE * 4);
+    m.out("prob", prob, SE * 4);
+    m.out("coef", coef, (int64_t(b.S) + 1) * 4);
+    m.out("workspace", ws, w.numel());
     MOE_CALL(r, moe_balance_loss(b.logits, b.T, b.E, b.idx, b.k, b.off, b.S, b.mask, loss, counts, prob, coef, ws, bytes,
                                  status, stream))
     return r;
@@ -246,6 +294,14 @@ PyObject* router_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const float* dloss = b.f32("dloss", a[7], 2, true);
     int32_t* status = b.i32("dev_status", a[10], 1, true);
     const cudaStream_t stream = stream_of(a[11], b.dev);
+    Memory m;
+    b.into(m);
+    m.in("gate", gate, Tk * 4);
+    m.in("dgate", dgate, Tk * 4);
+    m.in("counts", counts, static_cast<int64_t>(b.S) * b.E * 4);
+    m.in("coef", coef, (int64_t(b.S) + 1) * 4);
+    m.in("dloss", dloss, 8);
+    m.out("dlogits", dlogits, TE * 4);
     MOE_CALL(r, moe_router_backward(b.logits, b.T, b.E, b.idx, gate, dgate, b.k, b.off, b.S, b.mask, counts, coef, dloss,
                                     dlogits, status, stream))
     return r;
@@ -277,6 +333,15 @@ PyObject* combine_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     float* dy = f32("dy_perm", a[8], p * d, true);
     const int t = fits_int("T", T), kk = fits_int("k", k), dd = fits_int("d", d);
     const cudaStream_t stream = stream_of(a[9], dev);
+    Memory m;
+    m.in("y_perm", y, p * d * 4);
+    m.in("idx", id, p * 4);
+    m.in("gate", gate, p * 4);
+    m.in("inv_perm", inv, p * 4);
+    m.in("slot_of_expert", slot, int64_t(E) * 4);
+    m.in("dout", o, T * d * 4);
+    m.out("dgate", dg, p * 4);
+    m.out("dy_perm", dy, p * d * 4);
     MOE_CALL(r, moe_combine_backward(y, id, gate, inv, slot, o, t, kk, dd, E, dg, dy, stream))
     return r;
   });

@@ -274,3 +274,28 @@ def test_binding_refusals(moe):
         a.update(kw)
         with pytest.raises((ValueError, moe.MoeError)):
             moe.moe_linear_w4(**a)
+
+
+def test_out_overlaps_nothing_that_is_read(moe):
+    """x and out as columns of one buffer are apart; any common element is refused."""
+    N, K, T = 24, 64, 5
+    w, x = make("int4", 32, N, K, T, seed=15)
+    d = cuda(w)
+    buf = torch.empty((T, 96), dtype=torch.bfloat16, device="cuda")
+    buf[:, :K] = x.cuda()
+    want = torch.empty((T, N), dtype=torch.bfloat16, device="cuda")
+    args = dict(fmt="int4", group=32)
+    moe.moe_linear_w4(buf[:, :K], d["codes"], d["scales"], want, **args)
+    moe.moe_linear_w4(buf[:, :K], d["codes"], d["scales"], buf[:, 64:88], **args)
+    assert torch.equal(buf[:, 64:88], want) and torch.equal(buf[:, :K].cpu(), x)
+    for t, out in ((T, buf[:, 63:87]), (T, buf[:, :N]), (1, buf[:1, 8:32])):
+        with pytest.raises(ValueError, match="overlaps"):
+            moe.moe_linear_w4(buf[:t, :K], d["codes"], d["scales"], out, **args)
+    rows = torch.zeros((2 * T, 64), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError, match="overlaps"):                  # out's second row on x's first
+        moe.moe_linear_w4(rows[1:3], d["codes"], d["scales"], rows[:2, :N], **args)
+    with pytest.raises(ValueError, match="overlaps"):
+        moe.moe_linear_w4(buf[:1, :K], d["codes"], d["scales"], d["scales"].view(-1)[:N].view(1, N), **args)
+    moe.moe_linear_w4(rows[:0], d["codes"], d["scales"], rows[:0, :N], **args)
+    with pytest.raises((ValueError, moe.MoeError)):                    # no K at all
+        moe.moe_linear_w4(rows[:2, :0], d["codes"][:, :0], d["scales"][:, :0], want[:2], **args)

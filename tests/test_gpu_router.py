@@ -314,3 +314,27 @@ def test_binding_refusals(moe):
         moe.moe_router_backward(l, i, l.clone(), dgate=torch.zeros((4, 2), device="cuda"))
     with pytest.raises(ValueError):
         moe.moe_combine_backward(l, i, o[2], i, None, l, 8, o[2])
+
+
+def test_outputs_overlap_nothing_else_of_the_call(moe):
+    l, i = torch.zeros((4, 8), device="cuda"), torch.zeros((4, 2), dtype=torch.int32, device="cuda")
+    o = [torch.empty(2, device="cuda"), torch.empty((1, 8), dtype=torch.int32, device="cuda"),
+         torch.empty((1, 8), device="cuda"), torch.empty(2, device="cuda")]
+    ws = torch.empty(moe.moe_balance_loss_workspace_bytes(4, 8, 1), dtype=torch.uint8, device="cuda")
+    for bad in ((l.view(-1)[:2], *o[1:], ws), (o[0], i.view(1, 8), *o[2:], ws), (o[0], o[1], l[3:], o[3], ws),
+                (o[0], o[1], o[2], o[0], ws), (*o, l.view(torch.uint8).view(-1)), (o[2].view(-1)[:2], *o[1:], ws)):
+        with pytest.raises(ValueError, match="overlaps"):
+            moe.moe_balance_loss(l, i, *bad)
+    g = torch.zeros((4, 2), device="cuda")
+    with pytest.raises(ValueError, match="overlaps"):
+        moe.moe_router_backward(l, i, l, gate=g, dgate=g)
+    big = torch.zeros(40, device="cuda")
+    with pytest.raises(ValueError, match="overlaps"):
+        moe.moe_router_backward(l, i, big[:32].view(4, 8), gate=g, dgate=big[30:38].view(4, 2))
+    moe.moe_router_backward(l, i, big[:32].view(4, 8), gate=g, dgate=big[32:40].view(4, 2))
+    y, inv, dout = torch.zeros((8, 8), device="cuda"), torch.arange(8, dtype=torch.int32, device="cuda"), l
+    for dg, dy in ((g, None), (torch.empty_like(g), y), (y[0].view(4, 2), None), (y[0].view(4, 2), torch.empty_like(y))):
+        with pytest.raises(ValueError, match="overlaps"):
+            moe.moe_combine_backward(y, i, g, inv, None, dout, 8, dg, dy_perm=dy)
+    with pytest.raises(ValueError, match="overlaps"):
+        moe.moe_combine_backward(y, i, g, inv, None, y[:4], 8, torch.empty_like(g), dy_perm=y)
