@@ -9,13 +9,17 @@ namespace {
 
 // Which kernel: warp-level MMAs (linear_w4.cuh) or tcgen05 (linear_w4_tc.cuh,
 // linear_w4_tc16.cuh).  A tcgen05 tile of 128 rows is a chain of stages that takes
-// some 0.5 to 1 us a 1024 of K however few tokens it serves; many tokens, or enough
-// tiles to fill the SMs, pay for it.  Device time in us, warp / tcgen05, K = 4096:
-//   T = 8    N = 16384   INT4/128 15.3 / 17.4   MXFP4 24.8 / 26.2   NVFP4 23.0 / 30.3
-//   T = 16   N = 16384   INT4/128 23.8 / 17.7   INT4/32 28.3 / 29.2  MXFP4 30.5 / 26.3  NVFP4 27.8 / 30.3
-//            N = 131072  INT4/128  150 / 113    INT4/32  195 / 195   MXFP4  205 / 170   NVFP4  188 / 195
-//   T = 32   N = 4096    INT4/128 18.3 / 21.8   INT4/32 23.9 / 29.6  MXFP4 22.9 / 23.5  NVFP4 19.7 / 27.3
-//            N = 16384   INT4/128 27.6 / 22.2   INT4/32 43.8 / 30.0  MXFP4 44.5 / 24.1  NVFP4 38.7 / 27.7
+// 0.5 to 1 us a 1024 of K however few tokens it serves.  Above 16 tokens clusters
+// share that chain where tiles are few; up to 16, enough tiles to fill the SMs pay
+// for it.  Device time in us, warp / tcgen05, K = 4096 (weights of N <= 16384 in L2):
+//   T = 8    N = 16384   INT4/128 14.9 / 17.9   INT4/32 22.9 / 30.7  MXFP4 24.2 / 26.3  NVFP4 23.2 / 29.5
+//   T = 16   N = 4096    INT4/128  8.6 / 17.6   INT4/32 10.9 / 12.1  MXFP4 10.9 / 26.0  NVFP4  9.6 / 11.6
+//            N = 16384   INT4/128 23.2 / 18.0   INT4/32 28.1 / 31.0  MXFP4 29.6 / 26.4  NVFP4 28.3 / 29.5
+//            N = 131072  INT4/128  146 / 114    INT4/32  193 / 200   MXFP4  195 / 170   NVFP4  192 / 190
+//   T = 17   N = 1024    INT4/128 17.4 /  7.6   INT4/32 21.1 /  8.9  MXFP4 21.6 /  7.6  NVFP4 19.0 /  8.6
+//            N = 16384   INT4/128 26.9 / 23.2   INT4/32 30.8 / 30.8  MXFP4 32.0 / 25.6  NVFP4 30.6 / 29.6
+//   T = 64   N = 16384   INT4/128 52.1 / 26.8   INT4/32 84.3 / 38.5  MXFP4 86.0 / 27.4  NVFP4 76.2 / 31.7
+//   T = 512  N = 4096    INT4/128 90.8 / 38.5   INT4/32  148 / 51.8  MXFP4  150 / 32.1  NVFP4  133 / 38.0
 // MOE_LINEAR=warp|tc, read at every call, forces one.
 bool use_tc(const LinearParams& P, int fmt, int group, const DeviceInfo& dev) {
   const char* force = getenv("MOE_LINEAR");

@@ -24,6 +24,13 @@
 // each adds up, out of the others' shared memory and in their order, the sums of a
 // part of the tokens.
 //
+// Measured: T = 64, N = 16384, K = 4096, INT4 by 128: 25 us (344 TFLOP/s, 687 with
+// both planes; one set of eight warps took 44).  T = 1000, N = K = 4096 with SwiGLU:
+// 83 us (405, 810 with both planes; a stage takes 1330 cycles, its MMAs alone 1024).
+// T = 64, N = 1024: 8.8 us by clusters of 8.  What bounds it: at T <= 64 the instructions that
+// expand a stage (640 of its 1420 cycles, at two a clock for most of them) and the
+// latency of its hand-overs; above, the MMAs.
+//
 // Two sets of eight warps take the stages in turn, each with its own A buffer,
 // accumulators and MMA-issuing warp: the hand-overs of a stage (codes landed ->
 // expanded -> multiplied -> added up) cost more time than its work, and the sets'
@@ -37,6 +44,7 @@
 // frees its TMEM.
 #pragma once
 
+#include <atomic>
 #include <type_traits>
 
 #include "linear_w4.cuh"
@@ -582,28 +590,48 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int FMT, int GROUP, bool BF16, int NT, bool SHARED, bool RUNS>
-cudaError_t launch_tiles(const TcParams& Q, const CUtensorMap& tm_w, const CUtensorMap& tm_x, unsigned ctas,
+cudaError_t launch_tiles(TcParams Q, const CUtensorMap& tm_w, const CUtensorMap& tm_x, int64_t tiles,
                          const DeviceInfo& dev, cudaStream_t s) {
   using C = Cfg<FMT, GROUP, BF16, NT>;
   auto kern = linear_w4_tc_kernel<FMT, GROUP, BF16, NT, SHARED, RUNS>;
-  static bool done[64] = {};
-  if (!done[dev.id]) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-    if (e != cudaSuccess) return e;
-    done[dev.id] = true;
-  }
+  struct Device {
+    std::atomic<bool> ready;
+    int clusters[4];                          // that run side by side, of 1, 2, 4 and 8 CTAs
+  };
+  static Device devices[64];
+  Device& d = devices[dev.id];
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = s;
   cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = 1u << Q.ck_bits;
-  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-  cfg.attrs = at;
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  if (!d.ready.load(std::memory_order_acquire)) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    for (int b = 1; b <= 3 && SHARED; ++b) {
+      cfg.gridDim = dim3(1u << b);
+      at[0].val.clusterDim.x = 1u << b;
+      e = cudaOccupancyMaxActiveClusters(&d.clusters[b], kern, &cfg);
+      if (e != cudaSuccess) return e;
+    }
+    d.ready.store(true, std::memory_order_release);
+  }
+  // The most CTAs a tile that run side by side (the SMs of a GPC may not divide into
+  // clusters: 16 tiles in clusters of 8 took two turns, 22 us, at T = 256, N = 1024,
+  // K = 4096).
+  if (SHARED)
+    while (Q.ck_bits > 0 && tiles > d.clusters[Q.ck_bits]) --Q.ck_bits;
+  cfg.gridDim = dim3(static_cast<unsigned>(SHARED                ? tiles << Q.ck_bits
+                                           : tiles < dev.sm_count ? tiles
+                                                                  : dev.sm_count));
+  at[0].val.clusterDim.x = 1u << Q.ck_bits;
+  cfg.attrs = SHARED ? at : at + 1;
   cfg.numAttrs = SHARED ? 2 : 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tm_w, tm_x, Q);
   return e != cudaSuccess ? e : cudaGetLastError();
@@ -635,16 +663,13 @@ cudaError_t launch(const LinearParams& P, const DeviceInfo& dev, int32_t* status
   // four stages.
   const int nst = (P.K + KS - 1) / KS;
   while (Q.ck_bits < 3 && tiles << (Q.ck_bits + 1) <= dev.sm_count && nst >> (Q.ck_bits + 1) >= 4) ++Q.ck_bits;
-  const unsigned ctas = static_cast<unsigned>(Q.ck_bits > 0            ? tiles << Q.ck_bits
-                                              : tiles < dev.sm_count ? tiles
-                                                                     : dev.sm_count);
   if constexpr (!Cfg<FMT, GROUP, BF16, NT>::POST && NT == 128) {
     if (!P.y_f32)
-      return Q.ck_bits > 0 ? launch_tiles<FMT, GROUP, BF16, NT, true, false>(Q, tm_w, tm_x, ctas, dev, s)
-                           : launch_tiles<FMT, GROUP, BF16, NT, false, false>(Q, tm_w, tm_x, ctas, dev, s);
+      return Q.ck_bits > 0 ? launch_tiles<FMT, GROUP, BF16, NT, true, false>(Q, tm_w, tm_x, tiles, dev, s)
+                           : launch_tiles<FMT, GROUP, BF16, NT, false, false>(Q, tm_w, tm_x, tiles, dev, s);
   }
-  return Q.ck_bits > 0 ? launch_tiles<FMT, GROUP, BF16, NT, true, true>(Q, tm_w, tm_x, ctas, dev, s)
-                       : launch_tiles<FMT, GROUP, BF16, NT, false, true>(Q, tm_w, tm_x, ctas, dev, s);
+  return Q.ck_bits > 0 ? launch_tiles<FMT, GROUP, BF16, NT, true, true>(Q, tm_w, tm_x, tiles, dev, s)
+                       : launch_tiles<FMT, GROUP, BF16, NT, false, true>(Q, tm_w, tm_x, tiles, dev, s);
 }
 
 template <int FMT, int GROUP, bool BF16>

@@ -11,6 +11,11 @@
 // half the tokens of one of two groups); the quarters' sums meet in shared memory
 // at the end of a tile.
 //
+// Measured: T = 13, N = 128001, K = 4096, INT4 by 64, f16: 117 us, 2.4 TB/s, against
+// 156 on the warp-level kernel.  Bound by the expanding instructions and the
+// hand-overs of a stage (2080 cycles a 256 of K; its codes alone would take 800 at
+// the copy rate).
+//
 // Warps 0-15: workers; quadrant (TMEM lanes) = warp % 4; warps 0-7 expand the even
 // stages and 8-15 the odd ones, four warps a half of a stage's K.  Warp 16: TMA of
 // the codes, 17: of the token rows.  Warps 18, 19: MMAs of the even and odd stages.
