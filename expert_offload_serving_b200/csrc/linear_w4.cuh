@@ -58,7 +58,7 @@ struct LinearParams {
   int wm_bits;             // warps along the rows (log2); the warps left over split K
   int stages, ring;        // stages in flight + 1; slots (no more than there are stages)
   int x_rows;              // token rows a stage holds
-  int scale_vec;           // a thread's scales (and zeros) of a stage can be loaded at once
+  int scale_vec;           // rows of scales (and zeros) are aligned for loads of several groups
 };
 
 // Launchers, one per format family (linear_w4_int4.cu, linear_w4_fp4.cu).

@@ -84,6 +84,7 @@ struct Cfg {
   static constexpr int PLANES = BF16 && FMT == MOE_W_INT4 ? 2 : 1;     // bf16 values of a weight
   static constexpr int AC = PLANES * kACols;                           // TMEM columns of a set's A buffer
   static constexpr int GPS = POST ? KS / GROUP : 1;                    // accumulators of a stage
+  static constexpr int HC = FMT == MOE_W_NVFP4 ? 4 : GROUP == 32 ? 2 : 1;   // groups of half a stage
   static constexpr int ND = (512 - 2 * AC) / NT / 2 < 6 ? (512 - 2 * AC) / NT / 2 : 6;   // accumulators of a set
   static constexpr int XB = NT * 128;                                  // 64 elements of the token rows
   static constexpr int STAGE = kCodeBytes + 2 * XB;
@@ -144,6 +145,26 @@ __device__ __forceinline__ void tmem_load(uint32_t taddr, float (&v)[N]) {
   else if constexpr (N == 8) tmem_ld8(taddr, v);
   else if constexpr (N == 16) tmem_ld16(taddr, v);
   else tmem_ld32(taddr, v);
+}
+
+// N consecutive elements of type E at index i of p (aligned to N of them) by one load,
+// each masked and OR-ed.
+template <typename E, int N>
+__device__ __forceinline__ void load_groups(const void* p, size_t i, uint32_t (&v)[N], uint32_t keep, uint32_t mark) {
+  constexpr int B = sizeof(E) * N;
+  using V = typename std::conditional<
+      B == 1, uint8_t,
+      typename std::conditional<
+          B == 2, uint16_t,
+          typename std::conditional<B == 4, uint32_t, typename std::conditional<B == 8, uint2, uint4>::type>::type>::type>::type;
+  static_assert(sizeof(V) == B, "one load");
+  union {
+    V v;
+    E e[N];
+  } u;
+  u.v = __ldg(reinterpret_cast<const V*>(static_cast<const E*>(p) + i));
+#pragma unroll
+  for (int j = 0; j < N; ++j) v[j] = (u.e[j] & keep) | mark;
 }
 
 // A bounded wait for hand-overs that are due within a stage.  A look in vain is
@@ -348,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t c0 = srow * 64 + (((2 * half) ^ ((srow >> 1) & 3)) << 4);
     const uint32_t c1 = srow * 64 + (((2 * half + 1) ^ ((srow >> 1) & 3)) << 4);
     constexpr int CN = NT / 4;                                         // tokens of this thread
-    constexpr int HC = FMT == MOE_W_NVFP4 ? 4 : GROUP == 32 ? 2 : 1;   // groups of half a stage
+    constexpr int HC = C::HC;
     constexpr int HK = 64 / HC;                                        // K of one
     int base = 0, d[2] = {0, 0}, slot = set;                           // base: stages of the tiles before this one
     uint32_t dphase[2] = {0, 0}, aphase = 0, phase = 0;                // slot: of this set's next stage
@@ -365,31 +386,52 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int first = tile / Q.tt * per, tok0 = tile % Q.tt * NT;
       const int wrow = min(first + out_row, outs - 1) + (P.swiglu && lane >= 16 ? outs : 0);
       const size_t sbase = static_cast<size_t>(wrow) * P.groups;
-      // raw zeros and scales of a stage's half (0x10000 or more: there is one) ...
+      // Raw zeros and scales of a stage's half (0x10000 or more: there is one) ...  A
+      // load touches a line per lane, whatever its width, and the lines are what it
+      // costs: where rows are aligned for it (P.scale_vec), one takes all the groups.
       auto fetch_c = [&](int s, uint32_t (&z)[HC], uint32_t (&f)[HC]) {
+        const int g0 = ((s0 + s) * KS + half * 64) / GROUP;
 #pragma unroll
         for (int i = 0; i < HC; ++i) {
-          const int k = (s0 + s) * KS + half * 64 + i * HK;
           z[i] = 8u;
           f[i] = 0;
-          if (k >= P.K) continue;
-          const size_t at = sbase + k / GROUP;
-          if (FMT == MOE_W_INT4 && P.zeros != nullptr) z[i] = __ldg(P.zeros + at) & 15u;
-          if (FMT != MOE_W_INT4) f[i] = 0x10000u | __ldg(static_cast<const uint8_t*>(P.scales) + at);
-          else if (!C::POST && P.scale_type == MOE_DT_F32) f[i] = __ldg(static_cast<const uint32_t*>(P.scales) + at);
-          else if (!C::POST) f[i] = __ldg(static_cast<const uint16_t*>(P.scales) + at);
+        }
+        const size_t at = sbase + g0;
+        if (HC > 1 && P.scale_vec && g0 + HC <= P.groups) {
+          if (FMT == MOE_W_INT4 && P.zeros != nullptr) load_groups<uint8_t, HC>(P.zeros, at, z, 15u, 0u);
+          if (FMT != MOE_W_INT4) load_groups<uint8_t, HC>(P.scales, at, f, 255u, 0x10000u);
+          else if (!C::POST && P.scale_type == MOE_DT_F32) load_groups<uint32_t, HC>(P.scales, at, f, ~0u, 0u);
+          else if (!C::POST) load_groups<uint16_t, HC>(P.scales, at, f, 0xFFFFu, 0u);
+          return;
+        }
+#pragma unroll
+        for (int i = 0; i < HC; ++i) {
+          if (g0 + i >= P.groups) continue;
+          if (FMT == MOE_W_INT4 && P.zeros != nullptr) z[i] = __ldg(P.zeros + at + i) & 15u;
+          if (FMT != MOE_W_INT4) f[i] = 0x10000u | __ldg(static_cast<const uint8_t*>(P.scales) + at + i);
+          else if (!C::POST && P.scale_type == MOE_DT_F32) f[i] = __ldg(static_cast<const uint32_t*>(P.scales) + at + i);
+          else if (!C::POST) f[i] = __ldg(static_cast<const uint16_t*>(P.scales) + at + i);
         }
       };
       // ... and the scales of a whole stage's groups (POST)
       auto fetch_s = [&](int s, uint32_t (&f)[C::GPS]) {
+        const int g0 = (s0 + s) * C::GPS;
+#pragma unroll
+        for (int j = 0; j < C::GPS; ++j) f[j] = 0;
+        if (!C::POST) return;
+        const size_t at = sbase + g0;
+        if (C::GPS > 1 && P.scale_vec && g0 + C::GPS <= P.groups) {
+          if (FMT == MOE_W_MXFP4) load_groups<uint8_t, C::GPS>(P.scales, at, f, 255u, 0x10000u);
+          else if (P.scale_type == MOE_DT_F32) load_groups<uint32_t, C::GPS>(P.scales, at, f, ~0u, 0u);
+          else load_groups<uint16_t, C::GPS>(P.scales, at, f, 0xFFFFu, 0u);
+          return;
+        }
 #pragma unroll
         for (int j = 0; j < C::GPS; ++j) {
-          const int gi = (s0 + s) * C::GPS + j;
-          f[j] = 0;
-          if (!C::POST || gi >= P.groups) continue;
-          if (FMT == MOE_W_MXFP4) f[j] = 0x10000u | __ldg(static_cast<const uint8_t*>(P.scales) + sbase + gi);
-          else if (P.scale_type == MOE_DT_F32) f[j] = __ldg(static_cast<const uint32_t*>(P.scales) + sbase + gi);
-          else f[j] = __ldg(static_cast<const uint16_t*>(P.scales) + sbase + gi);
+          if (g0 + j >= P.groups) continue;
+          if (FMT == MOE_W_MXFP4) f[j] = 0x10000u | __ldg(static_cast<const uint8_t*>(P.scales) + at + j);
+          else if (P.scale_type == MOE_DT_F32) f[j] = __ldg(static_cast<const uint32_t*>(P.scales) + at + j);
+          else f[j] = __ldg(static_cast<const uint16_t*>(P.scales) + at + j);
         }
       };
       auto scale_of = [&](uint32_t r) {
@@ -645,6 +687,10 @@ cudaError_t launch(const LinearParams& P, const DeviceInfo& dev, int32_t* status
   Q.stall = test_stall();
   Q.status = status;
   Q.run_bits = P.y_f32 ? 3 : 30;
+  using C = Cfg<FMT, GROUP, BF16, NT>;
+  constexpr int A = C::GPS > C::HC ? C::GPS : C::HC;                   // groups that are loaded at once
+  const int e = FMT != MOE_W_INT4 ? 1 : P.scale_type == MOE_DT_F32 ? 4 : 2;
+  Q.L.scale_vec = A > 1 && P.groups % A == 0 && aligned(P.scales, A * e) && aligned(P.zeros, A);
   const int outs = P.swiglu ? P.N / 2 : P.N, per = P.swiglu ? TM / 2 : TM;
   Q.mt = (outs + per - 1) / per;
   Q.tt = (P.T + NT - 1) / NT;
@@ -663,7 +709,7 @@ cudaError_t launch(const LinearParams& P, const DeviceInfo& dev, int32_t* status
   // four stages.
   const int nst = (P.K + KS - 1) / KS;
   while (Q.ck_bits < 3 && tiles << (Q.ck_bits + 1) <= dev.sm_count && nst >> (Q.ck_bits + 1) >= 4) ++Q.ck_bits;
-  if constexpr (!Cfg<FMT, GROUP, BF16, NT>::POST && NT == 128) {
+  if constexpr (!C::POST && NT == 128) {
     if (!P.y_f32)
       return Q.ck_bits > 0 ? launch_tiles<FMT, GROUP, BF16, NT, true, false>(Q, tm_w, tm_x, tiles, dev, s)
                            : launch_tiles<FMT, GROUP, BF16, NT, false, false>(Q, tm_w, tm_x, tiles, dev, s);
