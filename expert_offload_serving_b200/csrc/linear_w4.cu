@@ -11,22 +11,28 @@ namespace {
 // linear_w4_tc16.cuh).  A tcgen05 tile of 128 rows is a chain of stages that takes
 // 0.5 to 1 us a 1024 of K however few tokens it serves.  Above 16 tokens clusters
 // share that chain where tiles are few; up to 16, enough tiles to fill the SMs pay
-// for it.  Device time in us, warp / tcgen05, K = 4096 (weights of N <= 16384 in L2):
-//   T = 8    N = 16384   INT4/128 14.9 / 17.9   INT4/32 22.9 / 30.7  MXFP4 24.2 / 26.3  NVFP4 23.2 / 29.5
-//   T = 16   N = 4096    INT4/128  8.6 / 17.6   INT4/32 10.9 / 12.1  MXFP4 10.9 / 26.0  NVFP4  9.6 / 11.6
-//            N = 16384   INT4/128 23.2 / 18.0   INT4/32 28.1 / 31.0  MXFP4 29.6 / 26.4  NVFP4 28.3 / 29.5
-//            N = 131072  INT4/128  146 / 114    INT4/32  193 / 200   MXFP4  195 / 170   NVFP4  192 / 190
-//   T = 17   N = 1024    INT4/128 17.4 /  7.6   INT4/32 21.1 /  8.9  MXFP4 21.6 /  7.6  NVFP4 19.0 /  8.6
-//            N = 16384   INT4/128 26.9 / 23.2   INT4/32 30.8 / 30.8  MXFP4 32.0 / 25.6  NVFP4 30.6 / 29.6
-//   T = 64   N = 16384   INT4/128 52.1 / 26.8   INT4/32 84.3 / 38.5  MXFP4 86.0 / 27.4  NVFP4 76.2 / 31.7
-//   T = 512  N = 4096    INT4/128 90.8 / 38.5   INT4/32  148 / 51.8  MXFP4  150 / 32.1  NVFP4  133 / 38.0
+// for it.  Groups of 32 whose sums are scaled (f16 x) have four hand-overs a stage,
+// which 32 tokens do not pay for either.  Device time in us, warp / tcgen05, K = 4096
+// (weights of N <= 16384 in L2):
+//   bf16 x               INT4/128      INT4/32       MXFP4         NVFP4         f16 x: INT4/32
+//   T = 8   N = 16384   14.5 / 17.8   22.7 / 25.7   24.3 / 26.4   22.9 / 25.5   22.7 / 44.5
+//   T = 16  N = 4096     9.0 / 17.6   10.9 / 10.6   10.8 / 26.0   10.0 / 10.1   10.8 / 15.5
+//           N = 16384   22.9 / 18.0   28.0 / 25.7   29.7 / 26.4   28.0 / 24.9   28.0 / 43.9
+//           N = 131072   146 / 114     193 / 167     195 / 170     192 / 162     193 / 304
+//   T = 17  N = 1024    17.5 /  7.5   21.1 /  7.8   21.8 /  7.6   19.0 /  7.4
+//           N = 4096    17.5 / 10.0   21.1 / 10.6   21.9 / 10.1   19.3 / 10.1   21.3 / 15.4
+//           N = 16384   26.9 / 22.7   30.7 / 25.5   32.2 / 24.7   30.4 / 24.8   30.5 / 43.9
+//           N = 131072   168 / 144     265 / 167     211 / 158     192 / 162     266 / 303
+//   T = 64  N = 16384   52.4 / 26.2   84.4 / 31.4   85.9 / 26.3   76.4 / 26.1    ..  / 60.5
+//   T = 512 N = 4096    91.0 / 37.4    148 / 42.6    151 / 30.9    133 / 31.4
 // MOE_LINEAR=warp|tc, read at every call, forces one.
-bool use_tc(const LinearParams& P, int fmt, int group, const DeviceInfo& dev) {
+bool use_tc(const LinearParams& P, int fmt, int group, bool bf16, const DeviceInfo& dev) {
   const char* force = getenv("MOE_LINEAR");
   if (force != nullptr) return strcmp(force, "tc") == 0;
-  if (P.T > 16) return true;
   const bool fills = P.N >= 77 * dev.sm_count;                 // 0.6 tiles of 128 rows for each SM
-  return P.T > 8 && fills && (fmt == MOE_W_MXFP4 || (fmt == MOE_W_INT4 && group >= 64));
+  const bool sums32 = !bf16 && group == 32 && !(fmt == MOE_W_MXFP4 && P.T <= 16);   // (those have a kernel)
+  if (P.T > 16) return !(sums32 && fills && P.T <= 32);
+  return P.T > 8 && fills && !sums32;
 }
 
 }  // namespace
@@ -84,7 +90,7 @@ extern "C" moe_status moe_linear_w4(moe_linear_shape s, const void* codes, const
   P.accumulate = (flags & MOE_LINEAR_ACCUMULATE) != 0;
   P.tensor_scale = tensor_scale;
   const bool bf16 = x_type == MOE_DT_BF16;
-  const bool tc = use_tc(P, s.fmt, s.group, dev);
+  const bool tc = use_tc(P, s.fmt, s.group, bf16, dev);
   const cudaError_t e = tc ? (int4 ? launch_linear_tc_int4(P, s.group, bf16, dev, dev_status, stream)
                                    : launch_linear_tc_fp4(P, s.fmt, bf16, dev, dev_status, stream))
                            : (int4 ? launch_linear_int4(P, s.group, bf16, dev, stream)

@@ -25,11 +25,14 @@
 // part of the tokens.
 //
 // Measured: T = 64, N = 16384, K = 4096, INT4 by 128: 25 us (344 TFLOP/s, 687 with
-// both planes; one set of eight warps took 44).  T = 1000, N = K = 4096 with SwiGLU:
-// 83 us (405, 810 with both planes; a stage takes 1330 cycles, its MMAs alone 1024).
-// T = 64, N = 1024: 8.8 us by clusters of 8.  What bounds it: at T <= 64 the instructions that
-// expand a stage (640 of its 1420 cycles, at two a clock for most of them) and the
-// latency of its hand-overs; above, the MMAs.
+// both planes; one set of eight warps took 44).  T = 1000, N = K = 4096 with SwiGLU,
+// INT4 by 32: 69 us (487, 974 with both planes), by 128 62 us.  T = 64, N = 1024: 8.7
+// us by clusters of 8.  A tile takes some 3 to 8 us beside its stages (first loads,
+// draining, epilogue), a stage of 64 tokens 1200 cycles and one of 128 1350 to 1550,
+// of which the two planes' MMAs are 512 and 1024 and the expanding instructions 640
+// (two a clock for most of them).  What bounds it is the hand-overs' latency: without
+// the second plane's MMAs T = 1000 took 14 % less, without the expanding arithmetic
+// 12 %, without both 26 %, without the loads of scales no less.
 //
 // Two sets of eight warps take the stages in turn, each with its own A buffer,
 // accumulators and MMA-issuing warp: the hand-overs of a stage (codes landed ->
