@@ -371,6 +371,16 @@ inline PFN_cuTensorMapEncodeTiled_v12000 encode_tiled_fn() {
   return fn;
 }
 
+// f(), once more on a thread to which no runtime call has bound the device's context
+// yet (a thread whose first CUDA work is this call): the driver's call needs it.
+template <typename F>
+inline CUresult with_context(F f) {
+  CUresult r = f();
+  int dev = 0;
+  if (r != CUDA_SUCCESS && cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess) r = f();
+  return r;
+}
+
 // A tiled map with 128-byte swizzle: dims/strides in elements/bytes (strides
 // of dims 1..rank-1), box in elements; no interleave, zero fill out of bounds.
 // Returns a CUresult (CUDA_ERROR_NOT_FOUND when the entry point is missing).
@@ -386,8 +396,10 @@ inline CUresult encode_tiled_sw128(CUtensorMap* map, CUtensorMapDataType type, i
     estr[i] = 1u;
   }
   for (int i = 0; i < rank - 1; ++i) gstr[i] = strides[i];
-  return fn(map, type, rank, const_cast<void*>(base), gdim, gstr, bx, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return with_context([&] {
+    return fn(map, type, rank, const_cast<void*>(base), gdim, gstr, bx, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  });
 }
 
 // The same with a 64-byte swizzle (inner box of 64 bytes).
@@ -403,8 +415,10 @@ inline CUresult encode_tiled_sw64(CUtensorMap* map, CUtensorMapDataType type, in
     estr[i] = 1u;
   }
   for (int i = 0; i < rank - 1; ++i) gstr[i] = strides[i];
-  return fn(map, type, rank, const_cast<void*>(base), gdim, gstr, bx, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return with_context([&] {
+    return fn(map, type, rank, const_cast<void*>(base), gdim, gstr, bx, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  });
 }
 
 // The same without swizzle (rows land at the box's own pitch).
@@ -420,8 +434,10 @@ inline CUresult encode_tiled_plain(CUtensorMap* map, CUtensorMapDataType type, i
     estr[i] = 1u;
   }
   for (int i = 0; i < rank - 1; ++i) gstr[i] = strides[i];
-  return fn(map, type, rank, const_cast<void*>(base), gdim, gstr, bx, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return with_context([&] {
+    return fn(map, type, rank, const_cast<void*>(base), gdim, gstr, bx, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  });
 }
 
 }  // namespace tc

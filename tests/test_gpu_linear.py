@@ -299,3 +299,55 @@ def test_out_overlaps_nothing_that_is_read(moe):
     moe.moe_linear_w4(rows[:0], d["codes"], d["scales"], rows[:0, :N], **args)
     with pytest.raises((ValueError, moe.MoeError)):                    # no K at all
         moe.moe_linear_w4(rows[:2, :0], d["codes"][:, :0], d["scales"][:, :0], want[:2], **args)
+
+
+@pytest.mark.parametrize("T", [5, 24, 100])
+def test_calls_at_once_from_two_threads(moe, T):
+    """Two threads, a stream each, over the same weights: every result has the bits of
+    a call alone."""
+    import threading
+    w, x = make("int4", 64, 1024, 2048, T, seed=16)
+    d, xs = cuda(w), x.cuda()
+    want = torch.empty((T, 1024), device="cuda")
+    call(moe, d, xs, want)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [[torch.full((T, 1024), -1.0, device="cuda") for _ in range(20)] for _ in streams]
+    torch.cuda.synchronize()
+    errors = []
+
+    def run(s, os):
+        try:
+            for o in os:
+                call(moe, d, xs, o, stream=s)
+        except Exception as e:                                         # raised below, on the test's thread
+            errors.append(e)
+    threads = [threading.Thread(target=run, args=a) for a in zip(streams, outs)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors
+    for o in outs[0] + outs[1]:
+        assert torch.equal(o, want)
+
+
+def test_the_first_call_of_a_process_can_be_captured(moe):
+    """Kernel attributes and the clusters' number are asked for inside the capture."""
+    import subprocess
+    import sys
+    code = ("import torch, expert_offload_serving_b200 as m\n"
+            "T, N, K = 24, 1024, 2048\n"
+            "x = torch.randn((T, K), device='cuda').to(torch.bfloat16)\n"
+            "c = torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, device='cuda')\n"
+            "s = torch.ones((N, K // 64), dtype=torch.bfloat16, device='cuda')\n"
+            "a, b = torch.zeros((T, N), device='cuda'), torch.zeros((T, N), device='cuda')\n"
+            "g = torch.cuda.CUDAGraph()\n"
+            "with torch.cuda.graph(g):\n"
+            "    m.moe_linear_w4(x, c, s, a, group=64)\n"
+            "g.replay()\n"
+            "m.moe_linear_w4(x, c, s, b, group=64)\n"
+            "torch.cuda.synchronize()\n"
+            "assert a.abs().max() > 0 and torch.equal(a, b)\n")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
