@@ -19,7 +19,7 @@ import time
 
 import torch
 
-from . import (LINEAR_FORMATS, MOE_FFN_ACT_NVFP4, FORMATS, MoeCache, _check, lib, moe_balance_loss,
+from . import (LINEAR_FORMATS, MOE_ERR_UNSUPPORTED, MOE_FFN_ACT_NVFP4, FORMATS, MoeCache, _check, lib, moe_balance_loss,
                moe_balance_loss_workspace_bytes, moe_combine_backward, moe_combine_merge, moe_expert_blob_bytes,
                moe_expert_ffn, moe_expert_ffn_workspace_bytes, moe_host_expert_ffn, moe_linear_w4, moe_pack_expert,
                moe_permute, moe_permute_scratch_bytes, moe_route_topk, moe_router_backward, moe_split_misses, shape)
@@ -178,6 +178,10 @@ class MoeLayer:
         self.y_perm = None if act == "nvfp4" else torch.empty((max(n, 1), d), **f32)
         self.out = torch.empty((T_max, d), **f32)
         self.status = torch.zeros((1,), **i32)
+        # The slots of the last step, for its gradient (_keep_slots); None: the table's own
+        self.step_slot = None
+        self._step_slot = None if act == "nvfp4" else torch.empty((E,), **i32)
+        self._host_steps = False             # whether any step (one that a graph replays, too) merged a host partial
         self.shared = shared
         if shared is not None:
             if shared.d != d or shared.a.shape[0] < T_max or shared.a.dtype != torch.bfloat16:
@@ -258,6 +262,25 @@ class MoeLayer:
                 rs = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
             self.xcache.reads_done.record(rs)
 
+    def _keep_slots(self, stream, host):
+        """The slot table as this step read it, for router_grad: later fills (of any
+        layer of the cache) change the table.  Only signs count there, so a step that
+        merged a host partial keeps twice the slots: an expert without one is marked
+        -2, as its outputs may be in the partial.  A resident layer's table stays, so
+        its plain steps copy nothing."""
+        if self._step_slot is None:
+            return
+        self._host_steps = self._host_steps or host
+        self.step_slot = None
+        if self.xcache is None and not host:
+            return
+        with self._memory_of(stream):
+            if host:
+                torch.mul(self.slot, 2, out=self._step_slot)
+            else:
+                self._step_slot.copy_(self.slot)
+        self.step_slot = self._step_slot
+
     def ffn(self, x, stream=None, out=None, host_partial=None):
         """The expert FFN.  act="nvfp4": the FFN adds gate-weighted outputs
         into `out` itself (fused combine), so `out` is first set to
@@ -292,7 +315,8 @@ class MoeLayer:
         self._check_tensor("host_partial", host_partial, (T, self.d), torch.float32)
         moe_combine_merge(self.y_perm, self.idx[:T], self.gate[:T], self.inv_perm, self.slot, host_partial,
                           self.E, out if out is not None else self.out[:T], stream)
-        self._record_reads_done(stream)              # combine reads the slot table
+        self._keep_slots(stream, host_partial is not None)
+        self._record_reads_done(stream)              # both read the slot table
 
     def split_step(self, step: int, logits, x, q=None, bw=(0.0, 0.0), threads: int = 0, stream=None):
         """One cached decode step whose misses are split between GPU fills and
@@ -385,6 +409,7 @@ class MoeLayer:
                               0 if self.y_perm is None else self.y_perm.data_ptr(), self.flags,
                               self.workspace.data_ptr(), nb(self.workspace))
         s = (torch.cuda.current_stream() if stream is None else stream)
+        host = host_partial is not None
         if self.shared is not None and T > 0:
             # the shared expert's sum (and the host's, if there is one) is the partial the combine adds
             so = self.shared_out[:T]
@@ -397,6 +422,7 @@ class MoeLayer:
         hp = 0 if host_partial is None else host_partial.data_ptr()
         _check(lib().moe_layer_forward(self.s, logits.data_ptr(), x.data_ptr(), T, self.k, *self._fwd_args, hp,
                                        self.out.data_ptr(), self.status.data_ptr(), s))
+        self._keep_slots(stream, host)
         self._record_reads_done(stream)
         return self.out[:T]
 
@@ -420,10 +446,18 @@ class MoeLayer:
 
     def router_grad(self, logits, dout=None, balance=None, dloss=None, seq_offsets=None, mask=None, stream=None):
         """d(loss)/d(logits) [T, E], the experts held fixed: of the layer's output
-        (dout [T, d], the gradient at forward()'s result; needs y_perm of the last
-        forward, so not act="nvfp4") and of the balance losses (balance: the dict
-        of balance(); dloss [2]: their weights).  Either part may be left out.  A new
-        tensor (of `stream`, if it is given)."""
+        (dout [T, d], the gradient at the result of the last forward(), combine() or
+        split_step(), which must have been of these tokens; needs y_perm of that step,
+        so not act="nvfp4") and of the balance losses (balance: the dict of balance();
+        dloss [2]: their weights).  Either part may be left out.  A new tensor (of
+        `stream`, if it is given).
+
+        The gates' gradient needs every chosen expert's output.  A step that left some
+        to the host (split_step, or a host_partial beside chosen experts that had no
+        slot) does not have them: dout is then refused (RuntimeError; in a graph that
+        is being captured, a replay records MOE_ERR_UNSUPPORTED in the status word).
+        A chosen expert that had no slot in a step without a host share was not part
+        of that step's output, and its gate's gradient is 0."""
         T = self._check_T(logits.shape[0])
         dgate = None
         if dout is not None:
@@ -432,9 +466,11 @@ class MoeLayer:
             self._check_tensor("dout", dout, (T, self.d), torch.float32)
             with self._memory_of(stream):
                 dgate = torch.empty((T, self.k), dtype=torch.float32, device=self.dev)
-            moe_combine_backward(self.y_perm, self.idx[:T], self.gate[:T], self.inv_perm, self.slot, dout, self.E, dgate,
+            if self._host_steps and self.step_slot is not None:
+                self._refuse_host_pairs(T, stream)
+            moe_combine_backward(self.y_perm, self.idx[:T], self.gate[:T], self.inv_perm,
+                                 self.slot if self.step_slot is None else self.step_slot, dout, self.E, dgate,
                                  stream=stream)
-            self._record_reads_done(stream)              # it reads the slot table, as combine does
         if (dloss is None) != (balance is None):
             raise ValueError("dloss and balance go together")
         b = balance or {}
@@ -444,6 +480,15 @@ class MoeLayer:
                             dgate=dgate, counts=b.get("counts"), coef=b.get("coef"), dloss=dloss,
                             seq_offsets=seq_offsets, mask=mask, dev_status=self.status, stream=stream)
         return dlogits
+
+    def _refuse_host_pairs(self, T, stream):
+        with self._memory_of(stream):
+            on_host = (self.step_slot[self.idx[:T].clamp(0, self.E - 1).long()] < -1).any()
+            if torch.cuda.is_current_stream_capturing():
+                self.status.masked_fill_(on_host & (self.status == 0), MOE_ERR_UNSUPPORTED)
+            elif on_host:
+                raise RuntimeError("the step left chosen experts to the host: their outputs, and with them the "
+                                   "gradient of its gates, are not here")
 
     @staticmethod
     def _memory_of(stream):
