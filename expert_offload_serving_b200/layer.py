@@ -428,12 +428,16 @@ class MoeLayer:
 
 
     # -- the router's training pass ------------------------------------------------
+    def _check_batch(self, logits, seq_offsets):
+        T = self._check_T(logits.shape[0])
+        self._check_tensor("logits", logits, (T, self.E), torch.float32)
+        return T, 1 if seq_offsets is None else seq_offsets.numel() - 1
+
     def balance(self, logits, seq_offsets=None, mask=None, stream=None):
         """The balance loss and statistics of the routing the last forward() (or
         route()) of these logits left in idx: dict(loss [2], counts [S, E], prob
         [S, E], coef [S + 1]), new tensors (of `stream`, if it is given)."""
-        T = self._check_T(logits.shape[0])
-        S = 1 if seq_offsets is None else seq_offsets.numel() - 1
+        T, S = self._check_batch(logits, seq_offsets)
         f32 = dict(dtype=torch.float32, device=self.dev)
         with self._memory_of(stream):
             r = dict(loss=torch.empty((2,), **f32), counts=torch.empty((S, self.E), dtype=torch.int32, device=self.dev),
@@ -458,7 +462,12 @@ class MoeLayer:
         is being captured, a replay records MOE_ERR_UNSUPPORTED in the status word).
         A chosen expert that had no slot in a step without a host share was not part
         of that step's output, and its gate's gradient is 0."""
-        T = self._check_T(logits.shape[0])
+        T, S = self._check_batch(logits, seq_offsets)
+        if (dloss is None) != (balance is None):
+            raise ValueError("dloss and balance go together")
+        b = balance or {}
+        self._check_tensor("counts", b.get("counts"), (S, self.E), torch.int32)
+        self._check_tensor("coef", b.get("coef"), (S + 1,), torch.float32)
         dgate = None
         if dout is not None:
             if self.y_perm is None:
@@ -471,9 +480,6 @@ class MoeLayer:
             moe_combine_backward(self.y_perm, self.idx[:T], self.gate[:T], self.inv_perm,
                                  self.slot if self.step_slot is None else self.step_slot, dout, self.E, dgate,
                                  stream=stream)
-        if (dloss is None) != (balance is None):
-            raise ValueError("dloss and balance go together")
-        b = balance or {}
         with self._memory_of(stream):
             dlogits = torch.empty((T, self.E), dtype=torch.float32, device=self.dev)
         moe_router_backward(logits, self.idx[:T], dlogits, gate=self.gate[:T] if dgate is not None else None,

@@ -181,3 +181,28 @@ def test_captured_step(moe):
     with pytest.raises(moe.MoeError) as e:
         moe.moe_check_status(layer.status)
     assert e.value.status == moe.MOE_ERR_UNSUPPORTED
+
+
+def test_logits_and_balance_of_another_shape_are_refused(moe):
+    """Narrower logits would leave results in the wrong columns; counts and coef of
+    other sequences would be read as this batch's."""
+    c = Cached()
+    layer, (logits, x, dout) = c.twins[0], c.in_[0]
+    layer.forward(logits, x)
+    dloss = torch.ones(2, device="cuda")
+    off = torch.tensor([0, 2, T], dtype=torch.int32, device="cuda")
+    bal, bal2 = layer.balance(logits), layer.balance(logits, seq_offsets=off)
+    for bad in (logits[:, :E // 2].contiguous(), torch.cat([logits, logits], 1), logits.double(), logits.cpu()):
+        with pytest.raises(ValueError, match="logits: expected a contiguous"):
+            layer.balance(bad)
+        with pytest.raises(ValueError, match="logits: expected a contiguous"):
+            layer.router_grad(bad, dout)
+        with pytest.raises(ValueError, match="logits: expected a contiguous"):
+            layer.router_grad(bad, balance=bal, dloss=dloss)
+    with pytest.raises(ValueError, match="counts"):
+        layer.router_grad(logits, balance=bal2, dloss=dloss)
+    with pytest.raises(ValueError, match="counts"):
+        layer.router_grad(logits, balance=bal, dloss=dloss, seq_offsets=off)
+    with pytest.raises(ValueError, match="coef"):
+        layer.router_grad(logits, balance=dict(bal, coef=bal2["coef"]), dloss=dloss)
+    layer.router_grad(logits, balance=bal2, dloss=dloss, seq_offsets=off)
