@@ -11,9 +11,9 @@ namespace {
 // linear_w4_tc16.cuh).  A tcgen05 tile of 128 rows is a chain of stages that takes
 // 0.5 to 1 us a 1024 of K however few tokens it serves.  Above 16 tokens clusters
 // share that chain where tiles are few; up to 16, enough tiles to fill the SMs pay
-// for it.  Groups of 32 whose sums are scaled (f16 x) have four hand-overs a stage,
-// which 32 tokens do not pay for either.  Device time in us, warp / tcgen05, K = 4096
-// (weights of N <= 16384 in L2):
+// for it.  Groups of 32 whose sums are scaled (f16 x; fp32 scales with an fp32 y) have
+// four hand-overs a stage, which 32 tokens do not pay for either.  Device time in us,
+// warp / tcgen05, K = 4096 (weights of N <= 16384 in L2):
 //   bf16 x               INT4/128      INT4/32       MXFP4         NVFP4         f16 x: INT4/32
 //   T = 8   N = 16384   14.5 / 17.8   22.7 / 25.7   24.3 / 26.4   22.9 / 25.5   22.7 / 44.5
 //   T = 16  N = 4096     9.0 / 17.6   10.9 / 10.6   10.8 / 26.0   10.0 / 10.1   10.8 / 15.5
@@ -30,7 +30,8 @@ bool use_tc(const LinearParams& P, int fmt, int group, bool bf16, const DeviceIn
   const char* force = getenv("MOE_LINEAR");
   if (force != nullptr) return strcmp(force, "tc") == 0;
   const bool fills = P.N >= 77 * dev.sm_count;                 // 0.6 tiles of 128 rows for each SM
-  const bool sums32 = !bf16 && group == 32 && !(fmt == MOE_W_MXFP4 && P.T <= 16);   // (those have a kernel)
+  const bool sums32 = scales_outside(P, fmt, bf16) && group == 32 &&
+                      !(fmt == MOE_W_MXFP4 && P.T <= 16);      // (those have a kernel)
   if (P.T > 16) return !(sums32 && fills && P.T <= 32);
   return P.T > 8 && fills && !sums32;
 }

@@ -61,6 +61,12 @@ struct LinearParams {
   int scale_vec;           // rows of scales (and zeros) are aligned for loads of several groups
 };
 
+// Whether the tcgen05 kernels multiply the groups' sums by the scales (see
+// linear_w4_tc.cuh) rather than the weights.
+inline bool scales_outside(const LinearParams& P, int fmt, bool bf16) {
+  return bf16 ? fmt == MOE_W_INT4 && P.scale_type == MOE_DT_F32 && P.y_f32 : fmt != MOE_W_NVFP4;
+}
+
 // Launchers, one per format family (linear_w4_int4.cu, linear_w4_fp4.cu).
 cudaError_t launch_linear_int4(const LinearParams& P, int group, bool bf16, const DeviceInfo& dev, cudaStream_t s);
 cudaError_t launch_linear_fp4(const LinearParams& P, int fmt, bool bf16, const DeviceInfo& dev, cudaStream_t s);

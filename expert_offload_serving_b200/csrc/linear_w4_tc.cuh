@@ -10,15 +10,20 @@
 //
 // Scales.  With bf16 x they go into the weights (PRE), and one fp32 accumulator
 // runs through all of K: an NVFP4 weight has 6 significant bits and an MXFP4 one
-// 2, exact in bf16; an INT4 weight (code - zero) * scale has up to 12 and becomes
-// the exact sum of two bf16 values, two A planes and two MMAs.  (A scale in fp16
-// or fp32 is itself taken as two bf16 values, and the weight is then within 2^-16.)
-// With f16 x, whose range does not hold every scale, INT4 and MXFP4 scales multiply
-// the group's fp32 sum (POST): the MMAs of a group write an accumulator of their
-// own, one of ND in turn, and the warps read it back and add it, scaled, to sums in
-// registers while the tensor core works on later groups.  The hand-overs that
-// takes cost more than the second plane: at T = 64, N = 16384, K = 4096 with groups
-// of 128, POST took 25 us in bf16.
+// 2, exact in bf16; an INT4 weight (code - zero) * scale has up to 12 with a bf16
+// scale and 15 with an fp16 one (two bf16 values itself), and becomes the exact sum
+// of two bf16 values, two A planes and two MMAs.  An fp32 scale leaves up to 28
+// bits: as two bf16 values the scale is within 2^-16, and two more roundings of the
+// product by 2^-16 leave the weight within 2^-14.8 of itself.  A 16-bit y takes
+// that, its own rounding is 2^-8; for an fp32 y these scales stay outside (T = 1000,
+// N = K = 4096: 64.5 us with groups of 128, 127 of 64, 194 of 32, where they took 71,
+// 76 and 82 inside; T = 24, N = 16384: 23.7, 30.5, 38.3 against 23.0, 23.9, 26.0).
+// With f16 x, whose range does not hold every scale, and in that case INT4 and MXFP4
+// scales multiply the group's fp32 sum (POST): the MMAs of a group write an
+// accumulator of their own, one of ND in turn, and the warps read it back and add
+// it, scaled, to sums in registers while the tensor core works on later groups.
+// The hand-overs that takes cost more than the second plane: at T = 64, N = 16384,
+// K = 4096 with groups of 128, POST took 25 us in bf16.
 //
 // Few tiles: a cluster of 2, 4 or 8 CTAs shares a tile, each with a part of K, and
 // each adds up, out of the others' shared memory and in their order, the sums of a
@@ -81,10 +86,14 @@ struct TcParams {
   int32_t* status;
 };
 
-template <int FMT, int GROUP, bool BF16, int NT>
+// Whether an x type has the scales outside the products of its own accord.
+template <int FMT, bool BF16>
+constexpr bool kPost = !BF16 && FMT != MOE_W_NVFP4;
+
+// POST: the scale multiplies a group's sum.
+template <int FMT, int GROUP, bool BF16, int NT, bool POST>
 struct Cfg {
-  static constexpr bool POST = !BF16 && FMT != MOE_W_NVFP4;            // the scale multiplies a group's sum
-  static constexpr int PLANES = BF16 && FMT == MOE_W_INT4 ? 2 : 1;     // bf16 values of a weight
+  static constexpr int PLANES = BF16 && FMT == MOE_W_INT4 && !POST ? 2 : 1;   // bf16 values of a weight
   static constexpr int AC = PLANES * kACols;                           // TMEM columns of a set's A buffer
   static constexpr int GPS = POST ? KS / GROUP : 1;                    // accumulators of a stage
   static constexpr int HC = FMT == MOE_W_NVFP4 ? 4 : GROUP == 32 ? 2 : 1;   // groups of half a stage
@@ -186,11 +195,11 @@ __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile
 // after each run.  (Instances of their own: the few more instructions of SHARED made
 // the loops of the other one 12 % slower at NT = 64, the sums that RUNS holds across
 // them 14 % at NT = 128.)
-template <int FMT, int GROUP, bool BF16, int NT, bool SHARED, bool RUNS>
+template <int FMT, int GROUP, bool BF16, int NT, bool POST, bool SHARED, bool RUNS>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
                         const __grid_constant__ TcParams Q) {
-  using C = Cfg<FMT, GROUP, BF16, NT>;
+  using C = Cfg<FMT, GROUP, BF16, NT, POST>;
   const LinearParams& P = Q.L;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -211,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int rank = SHARED ? static_cast<int>(cluster_rank()) : 0;
   const int all = (P.K + KS - 1) / KS, s0 = all * rank >> ck_bits, nst = (all * (rank + 1) >> ck_bits) - s0;
   const int ntiles = Q.mt * Q.tt, tile0 = blockIdx.x >> ck_bits, tiles_step = gridDim.x >> ck_bits;
-  const int run = C::POST ? 1 : 1 << (RUNS ? Q.run_bits : 30);
+  const int run = POST ? 1 : 1 << (RUNS ? Q.run_bits : 30);
   int meetings = 0;                           // barriers over the cluster: two, on every path
   const int outs = P.swiglu ? P.N >> 1 : P.N, per = P.swiglu ? TM / 2 : TM;   // outputs: in all, of a tile
 
@@ -318,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         aphase ^= 1u;
         const uint64_t xd = xdesc + (slot * C::STAGE >> 4);
         // the set's first and last stage of a run (of one stage, in POST)
-        const bool begin = C::POST || (s & (run - 1)) < 2, end = C::POST || (s & (run - 1)) >= run - 2 || s + 2 >= nst;
+        const bool begin = POST || (s & (run - 1)) < 2, end = POST || (s & (run - 1)) >= run - 2 || s + 2 >= nst;
 #pragma unroll
         for (int j = 0; j < C::GPS; ++j) {
           if (begin) {
@@ -403,8 +412,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (HC > 1 && P.scale_vec && g0 + HC <= P.groups) {
           if (FMT == MOE_W_INT4 && P.zeros != nullptr) load_groups<uint8_t, HC>(P.zeros, at, z, 15u, 0u);
           if (FMT != MOE_W_INT4) load_groups<uint8_t, HC>(P.scales, at, f, 255u, 0x10000u);
-          else if (!C::POST && P.scale_type == MOE_DT_F32) load_groups<uint32_t, HC>(P.scales, at, f, ~0u, 0u);
-          else if (!C::POST) load_groups<uint16_t, HC>(P.scales, at, f, 0xFFFFu, 0u);
+          else if (!POST && P.scale_type == MOE_DT_F32) load_groups<uint32_t, HC>(P.scales, at, f, ~0u, 0u);
+          else if (!POST) load_groups<uint16_t, HC>(P.scales, at, f, 0xFFFFu, 0u);
           return;
         }
 #pragma unroll
@@ -412,8 +421,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (g0 + i >= P.groups) continue;
           if (FMT == MOE_W_INT4 && P.zeros != nullptr) z[i] = __ldg(P.zeros + at + i) & 15u;
           if (FMT != MOE_W_INT4) f[i] = 0x10000u | __ldg(static_cast<const uint8_t*>(P.scales) + at + i);
-          else if (!C::POST && P.scale_type == MOE_DT_F32) f[i] = __ldg(static_cast<const uint32_t*>(P.scales) + at + i);
-          else if (!C::POST) f[i] = __ldg(static_cast<const uint16_t*>(P.scales) + at + i);
+          else if (!POST && P.scale_type == MOE_DT_F32) f[i] = __ldg(static_cast<const uint32_t*>(P.scales) + at + i);
+          else if (!POST) f[i] = __ldg(static_cast<const uint16_t*>(P.scales) + at + i);
         }
       };
       // ... and the scales of a whole stage's groups (POST)
@@ -421,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int g0 = (s0 + s) * C::GPS;
 #pragma unroll
         for (int j = 0; j < C::GPS; ++j) f[j] = 0;
-        if (!C::POST) return;
+        if (!POST) return;
         const size_t at = sbase + g0;
         if (C::GPS > 1 && P.scale_vec && g0 + C::GPS <= P.groups) {
           if (FMT == MOE_W_MXFP4) load_groups<uint8_t, C::GPS>(P.scales, at, f, 255u, 0x10000u);
@@ -497,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Stages up to s - 2 are added up before the wait for the buffer that stage
         // s - 2's MMAs read: these may in turn wait for accumulators (a stage can
         // have more groups than there are accumulators).
-        for (; (C::POST || RUNS) && next * run + run < s && ok; ++next) ok = C::POST ? add_up(next) : add_run(next);
+        for (; (POST || RUNS) && next * run + run < s && ok; ++next) ok = POST ? add_up(next) : add_run(next);
         uint32_t c[HC], s1[HC], s2[HC];
 #pragma unroll
         for (int i = 0; i < HC; ++i) {
@@ -506,8 +515,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             c[i] = sn[i] == 0 ? 0u : pair_constant<FMT, BF16>(sn[i] & 255u);
           } else {
             c[i] = pair_constant<FMT, BF16>(zn[i]);
-            if (!C::POST && FMT == MOE_W_MXFP4) s1[i] = sn[i] == 0 ? 0u : e8m0_quarter(sn[i] & 255u);
-            if (!C::POST && FMT == MOE_W_INT4) {
+            if (!POST && FMT == MOE_W_MXFP4) s1[i] = sn[i] == 0 ? 0u : e8m0_quarter(sn[i] & 255u);
+            if (!POST && FMT == MOE_W_INT4) {
               const float f = scale_of(sn[i]);
               const __nv_bfloat16 hi = __float2bfloat16_rn(f);
               s1[i] = __bfloat16_as_ushort(hi) * 0x10001u;
@@ -540,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             a[4 * e + 1] = natural_pair<FMT, BF16, 1>(w[i], up, c[h]);
             a[4 * e + 2] = natural_pair<FMT, BF16, 2>(w[i], up, c[h]);
             a[4 * e + 3] = natural_pair<FMT, BF16, 3>(w[i], up, c[h]);
-            if constexpr (!C::POST && FMT == MOE_W_MXFP4) {
+            if constexpr (!POST && FMT == MOE_W_MXFP4) {
 #pragma unroll
               for (int p = 4 * e; p < 4 * e + 4; ++p) a[p] = w4::mul2<true>(a[p], s1[h]);
             }
@@ -577,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         arrive(&afull[set]);
       }
-      for (; next * run < nst && ok; ++next) ok = C::POST ? add_up(next) : add_run(next);
+      for (; next * run < nst && ok; ++next) ok = POST ? add_up(next) : add_run(next);
       if (!ok) break;
       // y[t][n] of tokens i and i + 1 of this thread: lanes hold consecutive n
       const int n = first + out_row;
@@ -634,11 +643,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512));
 }
 
-template <int FMT, int GROUP, bool BF16, int NT, bool SHARED, bool RUNS>
+template <int FMT, int GROUP, bool BF16, int NT, bool POST, bool SHARED, bool RUNS>
 cudaError_t launch_tiles(TcParams Q, const CUtensorMap& tm_w, const CUtensorMap& tm_x, int64_t tiles,
                          const DeviceInfo& dev, cudaStream_t s) {
-  using C = Cfg<FMT, GROUP, BF16, NT>;
-  auto kern = linear_w4_tc_kernel<FMT, GROUP, BF16, NT, SHARED, RUNS>;
+  using C = Cfg<FMT, GROUP, BF16, NT, POST>;
+  auto kern = linear_w4_tc_kernel<FMT, GROUP, BF16, NT, POST, SHARED, RUNS>;
   struct Device {
     std::atomic<bool> ready;
     int clusters[4];                          // that run side by side, of 1, 2, 4 and 8 CTAs
@@ -682,7 +691,7 @@ cudaError_t launch_tiles(TcParams Q, const CUtensorMap& tm_w, const CUtensorMap&
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <int FMT, int GROUP, bool BF16, int NT>
+template <int FMT, int GROUP, bool BF16, int NT, bool POST>
 cudaError_t launch(const LinearParams& P, const DeviceInfo& dev, int32_t* status, cudaStream_t s) {
   TcParams Q{};
   Q.L = P;
@@ -690,7 +699,7 @@ cudaError_t launch(const LinearParams& P, const DeviceInfo& dev, int32_t* status
   Q.stall = test_stall();
   Q.status = status;
   Q.run_bits = P.y_f32 ? 3 : 30;
-  using C = Cfg<FMT, GROUP, BF16, NT>;
+  using C = Cfg<FMT, GROUP, BF16, NT, POST>;
   constexpr int A = C::GPS > C::HC ? C::GPS : C::HC;                   // groups that are loaded at once
   const int e = FMT != MOE_W_INT4 ? 1 : P.scale_type == MOE_DT_F32 ? 4 : 2;
   Q.L.scale_vec = A > 1 && P.groups % A == 0 && aligned(P.scales, A * e) && aligned(P.zeros, A);
@@ -712,20 +721,20 @@ cudaError_t launch(const LinearParams& P, const DeviceInfo& dev, int32_t* status
   // four stages.
   const int nst = (P.K + KS - 1) / KS;
   while (Q.ck_bits < 3 && tiles << (Q.ck_bits + 1) <= dev.sm_count && nst >> (Q.ck_bits + 1) >= 4) ++Q.ck_bits;
-  if constexpr (!C::POST && NT == 128) {
+  if constexpr (!POST && NT == 128) {
     if (!P.y_f32)
-      return Q.ck_bits > 0 ? launch_tiles<FMT, GROUP, BF16, NT, true, false>(Q, tm_w, tm_x, tiles, dev, s)
-                           : launch_tiles<FMT, GROUP, BF16, NT, false, false>(Q, tm_w, tm_x, tiles, dev, s);
+      return Q.ck_bits > 0 ? launch_tiles<FMT, GROUP, BF16, NT, POST, true, false>(Q, tm_w, tm_x, tiles, dev, s)
+                           : launch_tiles<FMT, GROUP, BF16, NT, POST, false, false>(Q, tm_w, tm_x, tiles, dev, s);
   }
-  return Q.ck_bits > 0 ? launch_tiles<FMT, GROUP, BF16, NT, true, true>(Q, tm_w, tm_x, tiles, dev, s)
-                       : launch_tiles<FMT, GROUP, BF16, NT, false, true>(Q, tm_w, tm_x, tiles, dev, s);
+  return Q.ck_bits > 0 ? launch_tiles<FMT, GROUP, BF16, NT, POST, true, true>(Q, tm_w, tm_x, tiles, dev, s)
+                       : launch_tiles<FMT, GROUP, BF16, NT, POST, false, true>(Q, tm_w, tm_x, tiles, dev, s);
 }
 
-template <int FMT, int GROUP, bool BF16>
+template <int FMT, int GROUP, bool BF16, bool POST = kPost<FMT, BF16>>
 cudaError_t launch_tokens(const LinearParams& P, const DeviceInfo& dev, int32_t* status, cudaStream_t s) {
-  if (P.T <= 32) return launch<FMT, GROUP, BF16, 32>(P, dev, status, s);
-  if (P.T <= 64) return launch<FMT, GROUP, BF16, 64>(P, dev, status, s);
-  return launch<FMT, GROUP, BF16, 128>(P, dev, status, s);
+  if (P.T <= 32) return launch<FMT, GROUP, BF16, 32, POST>(P, dev, status, s);
+  if (P.T <= 64) return launch<FMT, GROUP, BF16, 64, POST>(P, dev, status, s);
+  return launch<FMT, GROUP, BF16, 128, POST>(P, dev, status, s);
 }
 
 }  // namespace w4tc

@@ -11,6 +11,9 @@ cudaError_t launch(const LinearParams& P, const DeviceInfo& dev, int32_t* status
   if constexpr (FMT == MOE_W_MXFP4 || (FMT == MOE_W_INT4 && GROUP >= 64)) {
     if (P.T <= w4t16::NT) return w4t16::launch<FMT, GROUP, BF16>(P, dev, status, s);
   }
+  if constexpr (BF16) {
+    if (scales_outside(P, MOE_W_INT4, true)) return w4tc::launch_tokens<FMT, GROUP, true, true>(P, dev, status, s);
+  }
   return w4tc::launch_tokens<FMT, GROUP, BF16>(P, dev, status, s);
 }
 

@@ -451,9 +451,10 @@ moe_status moe_profile_bandwidth(moe_shape s, const void* host_pool, int n_blobs
  *            values silu(h) * u.  With MOE_LINEAR_ACCUMULATE y += instead.
  *            Elements of y outside these rows are left as they were; y may not
  *            overlap x or the weights.
- * Products are exact (with bf16 x and INT4 scales in fp16 or fp32, within 2^-16 of
- * the weight on the tcgen05 kernels), sums are fp32 in a fixed order (the same call
- * gives the same bits), y is rounded once.  (The tensor cores cut off where fp32
+ * Products are exact, sums are fp32 in a fixed order (the same call gives the same
+ * bits), y is rounded once.  (Two exceptions on the tcgen05 kernels, INT4 with bf16 x:
+ * for a bf16 y, fp32 scales leave a weight within 2^-14.8 of itself; and unless the
+ * scales are fp32 and y is too, a weight above 2^127 may count as infinite.)  (The tensor cores cut off where fp32
  * would round: 2.4e-6 of the result's norm at K = 16384, measured.  For an fp32 y
  * the kernels therefore add up in registers after at most 1024 of K; for a 16-bit
  * y, whose own rounding is 100 times that, some sums run through all of K.)  An infinity or NaN

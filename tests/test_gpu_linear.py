@@ -351,3 +351,24 @@ def test_the_first_call_of_a_process_can_be_captured(moe):
             "assert a.abs().max() > 0 and torch.equal(a, b)\n")
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr
+
+
+@pytest.mark.parametrize("path", ["warp", "tc"])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_fp32_scales_keep_their_bits_for_an_fp32_y(moe, monkeypatch, path, group):
+    """bf16 x, fp32 scales: exact products and fp32 sums on both kernels.  At K = 4096
+    the up to 8 additions of a group cut off up to a step of 2^-23 each, half of that
+    on average: 8 2^-24 = 4.8e-7 of the group's sum and so of the whole (the groups'
+    signs are random); 32 to 128 fp32 roundings of the running sum, each up to 2^-24,
+    add as random errors do, at most sqrt(128 / 3) 2^-24 = 3.9e-7.  Below 1e-6 in norm
+    together.  (A weight within 2^-14.8 of itself, 2^-16 on average, would be off by
+    more than that.)"""
+    monkeypatch.setenv("MOE_LINEAR", path)
+    for T in (5, 24, 64, 130):
+        w, x = make("int4", group, 200, 4096, T, zeros=True, scale="f32", seed=17)
+        out = torch.empty((T, 200), device="cuda")
+        call(moe, cuda(w), x.cuda(), out)
+        check(out, w, x, "f32")
+        ref = O.linear(x.double().numpy(), oracle_weights(w))
+        norm = np.linalg.norm(out.double().cpu().numpy() - ref) / np.linalg.norm(ref)
+        assert norm <= 1e-6, (T, norm)
