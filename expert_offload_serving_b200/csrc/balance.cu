@@ -175,7 +175,8 @@ __device__ __forceinline__ RowStat softmax_row(float (&v)[VPL]) {
   RowStat r;
   r.top = top;
   r.inv = empty ? 0.f : __fdividef(1.f, sum);       // 1 <= sum <= E: within 2^-23 and 2^-21
-  r.lse = empty ? 0.f : top + __logf(sum);
+  // log in full: a z-loss drives lse to 0, where __logf's 2^-21 would be all of it
+  r.lse = empty ? 0.f : top + logf(sum);
   return r;
 }
 

@@ -338,3 +338,27 @@ def test_outputs_overlap_nothing_else_of_the_call(moe):
             moe.moe_combine_backward(y, i, g, inv, None, dout, 8, dg, dy_perm=dy)
     with pytest.raises(ValueError, match="overlaps"):
         moe.moe_combine_backward(y, i, g, inv, None, y[:4], 8, torch.empty_like(g), dy_perm=y)
+
+
+@pytest.mark.parametrize("T", [40, 300])
+def test_z_loss_of_rows_whose_logsumexp_is_near_zero(moe, T):
+    """A z-loss drives lse = max + log(sum) to 0, where only absolute errors are left.
+    E equal logits near -log E: the sum is E exactly and log is off by a step of its
+    value at most.  Logits 0 and -a: the sum 1 + exp(-a) is off by half a step of 1,
+    2^-24, and 2^-20 of the exponential; log passes that on.  The z-loss is lse^2 within
+    a few 2^-23 and its gradient 2 lse p / T within 2^-20 more (p)."""
+    rows = [(np.full(E, -np.log(E) + 1e-4), lambda l: np.spacing(np.float32(np.log(len(l))))) for E in range(3, 40)]
+    rows += [(np.array([0.0, -a]), lambda l: 2.0 ** -24 + 2.0 ** -20 * np.exp(l[1])) for a in np.linspace(2.0, 12.0, 21)]
+    for row, err in rows:
+        l = np.repeat(row.astype(np.float32)[None], T, 0)
+        idx = np.zeros((T, 1), dtype=np.int32)
+        o = run_balance(moe, l, idx)
+        r = l[0].astype(np.float64)
+        lse = np.log(np.exp(r).sum())
+        off = float(err(r)) + 2.0 ** -22 * abs(lse)
+        z = float(o["loss"][1].double().cpu())
+        assert abs(np.sqrt(z) - abs(lse)) <= off, (row[:2], np.sqrt(z) - abs(lse), off)
+        d = run_router(moe, l, idx, counts=o["counts"].cpu().numpy(), coef=o["coef"].cpu().numpy(),
+                       dloss=np.array([0.0, 1.0], dtype=np.float32))
+        p = np.exp(r - lse)
+        assert (np.abs(d.double().cpu().numpy() - 2 * lse * p / T) <= (2 * off + 2.0 ** -20 * abs(lse)) * p / T).all()
