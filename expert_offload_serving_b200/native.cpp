@@ -207,6 +207,20 @@ PyObject* linear_w4(PyObject*, PyObject* const* a, Py_ssize_t n) {
     m.in("codes", pc, codes.numel());
     m.in("scales", ps, scales.numel() * scales.element_size());
     if (zeros != nullptr) m.in("zeros", pz, zeros->numel());
+    // the status word may lie between the rows of x and out
+    auto in_rows = [&](const at::Tensor& r, int64_t bytes, int64_t step, int64_t width) {
+      const int64_t at = reinterpret_cast<char*>(status) - static_cast<char*>(r.data_ptr());
+      return at > -4 && at < bytes && (at < 0 || at % step < width || at % step + 4 > step);
+    };
+    if (status != nullptr && T > 0) {
+      if (in_rows(out, yb, ldy * ye, yw)) refuse("dev_status overlaps out");
+      if (in_rows(x, xb, pitch, K * xe)) refuse("dev_status overlaps x");
+      Memory w;
+      w.in("codes", pc, codes.numel());
+      w.in("scales", ps, scales.numel() * scales.element_size());
+      if (zeros != nullptr) w.in("zeros", pz, zeros->numel());
+      w.out("dev_status", status, 4);
+    }
     MOE_CALL(r, moe_linear_w4(s, pc, ps, static_cast<const uint8_t*>(pz), static_cast<float>(ts), x.data_ptr(), xt, ldx,
                               t, out.data_ptr(), yt, ldy, flags, status, stream))
     return r;
@@ -275,6 +289,7 @@ PyObject* balance_loss(PyObject*, PyObject* const* a, Py_ssize_t n) {
     m.out("prob", prob, SE * 4);
     m.out("coef", coef, (int64_t(b.S) + 1) * 4);
     m.out("workspace", ws, w.numel());
+    m.out("dev_status", status, 4);
     MOE_CALL(r, moe_balance_loss(b.logits, b.T, b.E, b.idx, b.k, b.off, b.S, b.mask, loss, counts, prob, coef, ws, bytes,
                                  status, stream))
     return r;
@@ -302,6 +317,7 @@ PyObject* router_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     m.in("coef", coef, (int64_t(b.S) + 1) * 4);
     m.in("dloss", dloss, 8);
     m.out("dlogits", dlogits, TE * 4);
+    m.out("dev_status", status, 4);
     MOE_CALL(r, moe_router_backward(b.logits, b.T, b.E, b.idx, gate, dgate, b.k, b.off, b.S, b.mask, counts, coef, dloss,
                                     dlogits, status, stream))
     return r;

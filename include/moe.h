@@ -450,7 +450,7 @@ moe_status moe_profile_bandwidth(moe_shape s, const void* host_pool, int n_blobs
  *            of W give h and rows N/2..N-1 give u, and a row of y is the N/2
  *            values silu(h) * u.  With MOE_LINEAR_ACCUMULATE y += instead.
  *            Elements of y outside these rows are left as they were; y may not
- *            overlap x or the weights.
+ *            overlap x or the weights, nor dev_status any of them.
  * Products are exact, sums are fp32 in a fixed order (the same call gives the same
  * bits), y is rounded once.  (Two exceptions on the tcgen05 kernels, INT4 with bf16 x:
  * for a bf16 y, fp32 scales leave a weight within 2^-14.8 of itself; and unless the
@@ -499,7 +499,7 @@ moe_status moe_linear_w4(moe_linear_shape s, const void* codes, const void* scal
  *     are offsets that decrease or leave [0, T] (the results are then undefined).
  *   workspace: device, 16-byte aligned, >= moe_balance_loss_workspace_bytes(T, E, S)
  *     bytes, contents need no set-up; calls that overlap in time need one each.
- *   Outputs and workspace overlap neither one another nor an input.
+ *   Outputs, workspace and status word overlap neither one another nor an input.
  * Limits as moe_route_topk; 1 <= S <= 1 << 20, 0 for arguments outside them. */
 size_t moe_balance_loss_workspace_bytes(int T, int E, int S);
 moe_status moe_balance_loss(const float* logits, int T, int E, const int32_t* idx, int k,
@@ -516,7 +516,10 @@ moe_status moe_balance_loss(const float* logits, int T, int E, const int32_t* id
  *   dloss: device fp32 [2], or NULL: no loss terms (counts and coef are not read).
  *   dgate: device fp32 [T][k], or NULL: no gate term (gate is not read); idx, gate:
  *   moe_route_topk's.  counts, coef, seq_offsets, S, mask, logits: as above.
- *   dlogits: device fp32 [T][E], overwritten; it overlaps no input. */
+ *   dlogits: device fp32 [T][E], overwritten; it overlaps no input.
+ *   dev_status: with a gate term, an id outside [0, E) is recorded as above and its
+ *   pair dropped.  Offsets are not looked over here (moe_balance_loss records bad
+ *   ones); bad ones lead no access astray, but the results are undefined. */
 moe_status moe_router_backward(const float* logits, int T, int E, const int32_t* idx, const float* gate,
                                const float* dgate, int k, const int32_t* seq_offsets, int S,
                                const uint8_t* mask, const int32_t* counts, const float* coef,

@@ -362,3 +362,35 @@ def test_z_loss_of_rows_whose_logsumexp_is_near_zero(moe, T):
                        dloss=np.array([0.0, 1.0], dtype=np.float32))
         p = np.exp(r - lse)
         assert (np.abs(d.double().cpu().numpy() - 2 * lse * p / T) <= (2 * off + 2.0 ** -20 * abs(lse)) * p / T).all()
+
+
+def test_the_status_word_lies_apart_from_the_outputs(moe):
+    """dev_status is written by a call, too: it may lie in nothing that the call reads
+    or writes."""
+    l, i = torch.zeros((4, 8), device="cuda"), torch.zeros((4, 2), dtype=torch.int32, device="cuda")
+    o = [torch.empty(2, device="cuda"), torch.empty((1, 8), dtype=torch.int32, device="cuda"),
+         torch.empty((1, 8), device="cuda"), torch.empty(2, device="cuda")]
+    ws = torch.empty(moe.moe_balance_loss_workspace_bytes(4, 8, 1), dtype=torch.uint8, device="cuda")
+    for st in (o[1].view(-1)[3:4], o[2].view(torch.int32).view(-1)[:1], ws[16:20].view(torch.int32), i.view(-1)[7:],
+               l.view(torch.int32).view(-1)[:1]):
+        with pytest.raises(ValueError, match="dev_status overlaps"):
+            moe.moe_balance_loss(l, i, *o, ws, dev_status=st)
+    g, dl = torch.zeros((4, 2), device="cuda"), torch.zeros((4, 8), device="cuda")
+    for st in (dl.view(torch.int32).view(-1)[31:], g.view(torch.int32).view(-1)[:1]):
+        with pytest.raises(ValueError, match="dev_status overlaps"):
+            moe.moe_router_backward(l, i, dl, gate=g, dgate=torch.zeros_like(g), dev_status=st)
+    x = torch.zeros((2, 64), dtype=torch.bfloat16, device="cuda")
+    c, s = torch.zeros((16, 32), dtype=torch.uint8, device="cuda"), torch.ones((16, 2), dtype=torch.bfloat16, device="cuda")
+    wide = torch.zeros((2, 24), device="cuda")
+    for st in (wide.view(torch.int32).view(-1)[25:26], x.view(torch.int32).view(-1)[:1], c.view(-1)[:4].view(torch.int32),
+               s.view(-1)[:2].view(torch.int32)):
+        with pytest.raises(ValueError, match="dev_status overlaps"):
+            moe.moe_linear_w4(x, c, s, wide[:, :16], group=32, dev_status=st)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    moe.moe_balance_loss(l, i, *o, ws, dev_status=st)
+    moe.moe_router_backward(l, i, dl, gate=g, dgate=torch.zeros_like(g), dev_status=st)
+    moe.moe_linear_w4(x, c, s, wide[:, :16], group=32, dev_status=st)
+    moe.moe_check_status(st)
+    gap = wide.view(torch.int32).view(-1)[16:17]                       # between out's rows
+    moe.moe_linear_w4(x, c, s, wide[:, :16], group=32, dev_status=gap)
+    moe.moe_check_status(gap)
