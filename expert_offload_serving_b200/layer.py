@@ -326,10 +326,10 @@ class MoeLayer:
 
         route -> read the routing back -> split the misses (moe_split_misses:
         q in [0, 1], or q=None for q* from bw = (pcie GB/s, host GB/s)) ->
-        fill the GPU share on the side stream -> permute + FFN on `stream`
-        while a CPU thread runs moe_host_expert_ffn over the host share ->
-        upload the host partial -> combine.  Returns the step's split
-        (hits, filled, host, fills) and the host kernel's wall time (host_ms)."""
+        fill the GPU share on the side stream -> permute + FFN (and the shared
+        expert) on `stream` while a CPU thread runs moe_host_expert_ffn over the
+        host share -> upload the host partial -> combine.  Returns the step's split
+        (hits, filled, host, fills) and the host kernel's wall time (host_ms).""""""
         if self.cache is None or self.act == "nvfp4":
             raise RuntimeError("split_step needs cached mode and the unfused FFN")
         T = self._check_T(x.shape[0])
@@ -375,17 +375,22 @@ class MoeLayer:
         th = threading.Thread(target=host_share) if host else None
         if th is not None:
             th.start()
-        self.permute(T, stream=s)
-        self.ffn(x, stream=s)
+        partial = None
+        try:
+            self.permute(T, stream=s)
+            self.ffn(x, stream=s)
+            if self.shared is not None:
+                partial = self.shared.add(x, self.shared_out[:T], accumulate=False, dev_status=self.status, stream=s)
+        finally:
+            if th is not None:
+                th.join()
         if th is not None:
-            th.join()
             if err:
                 raise err[0]
             with torch.cuda.stream(s):
-                b["hp_dev"][:T].copy_(b["hp"][:T], non_blocking=True)
-        if self.shared is not None:
-            self.shared.add(x, b["hp_dev"][:T], accumulate=bool(host), dev_status=self.status, stream=s)
-        self.combine(T, host_partial=b["hp_dev"][:T] if host or self.shared is not None else None, stream=s)
+                hp = b["hp_dev"][:T].copy_(b["hp"][:T], non_blocking=True)
+                partial = hp if partial is None else hp.add_(partial)
+        self.combine(T, host_partial=partial, stream=s)
         return dict(hits=hits, filled=filled, host=host, fills=fills, host_ms=host_ms[0])
 
     def forward(self, logits, x, host_partial=None, stream=None):

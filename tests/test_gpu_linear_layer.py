@@ -294,3 +294,33 @@ def test_captured_step_with_shared_expert_and_router_gradient(moe):
         for a, c in zip(want, captured):
             assert torch.equal(a, c)
     del eager
+
+
+def test_split_step_runs_the_shared_expert_beside_the_host_share(moe, monkeypatch):
+    """The shared expert needs only x, so its products are on the stream before the CPU
+    share is waited for.  The host's kernel stands in here for a slow one: it waits
+    (10 s at most) until the shared expert has been enqueued."""
+    import threading
+
+    from expert_offload_serving_b200 import layer as L
+    cfg = synth.LayerConfig("shared_split", E=16, k=4, d=512, I=256, fmt="mxfp4", bias_std=0.5, n_slots=12)
+    w = synth.make_experts(cfg, range(16), 8, device="cpu")
+    sh, _, _ = shared_expert("int4", 128, 512, 256, 3, seed=9)
+    layer = L.MoeLayer(16, 512, 256, "mxfp4", 4, 3, host_pool=L.pack_pool(16, 512, 256, "mxfp4", w, range(16)), n_slots=12,
+                       shared=sh)
+    logits, x = synth.make_routing(cfg, 3, 20)
+    enqueued, seen = threading.Event(), []
+    add, host = sh.add, L.moe_host_expert_ffn
+
+    def add_and_tell(*a, **kw):
+        r = add(*a, **kw)
+        enqueued.set()
+        return r
+
+    def slow_host(*a, **kw):
+        seen.append(enqueued.wait(10))
+        return host(*a, **kw)
+    monkeypatch.setattr(sh, "add", add_and_tell)
+    monkeypatch.setattr(L, "moe_host_expert_ffn", slow_host)
+    assert layer.split_step(0, logits.cuda(), x.cuda(), q=0.0, threads=2)["host"]
+    assert seen == [True]
