@@ -329,7 +329,7 @@ class MoeLayer:
         fill the GPU share on the side stream -> permute + FFN (and the shared
         expert) on `stream` while a CPU thread runs moe_host_expert_ffn over the
         host share -> upload the host partial -> combine.  Returns the step's split
-        (hits, filled, host, fills) and the host kernel's wall time (host_ms).""""""
+        (hits, filled, host, fills) and the host kernel's wall time (host_ms)."""
         if self.cache is None or self.act == "nvfp4":
             raise RuntimeError("split_step needs cached mode and the unfused FFN")
         T = self._check_T(x.shape[0])
