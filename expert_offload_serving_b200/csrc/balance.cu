@@ -14,8 +14,8 @@
 // experts), and its last CTA forms the loss.  Every sum has a fixed order; the
 // atomics only count (integers) or hand out tickets.
 //
-// Up to 128 tokens one CTA does it all (5.9 us at T = 64, E = 128, k = 8): the
-// latency of its steps bounds it.  T = 50000, E = 256, k = 6 in 29 sequences, a tenth
+// Few tokens of one sequence: one CTA does it all (5.3 us at T = 64, E = 128, k = 8);
+// the latency of its steps bounds it.  T = 50000, E = 256, k = 6 in 29 sequences, a tenth
 // masked: 20.7 us (2.3 TB/s), some 13 in the first kernel, bound by instructions (a
 // softmax and the sums of 8 values a lane), the rest the second one's chain of
 // dependent loads.  Cut into 592 tiles 23.9 us, 296 25.9, 1184 24.2 (with the calls'
@@ -302,17 +302,23 @@ __device__ V block_sum(V v, V* sh) {
   return s;
 }
 
-// One CTA does it all where the tokens are few: a second launch would cost more
-// than the whole sum.  Sequences one after the other; the loss and the factors,
-// which need the number of sequences with tokens, at the end.
-constexpr int kSmallTokens = 128;
+// One CTA does it all where one sequence has few tokens: a second launch would cost
+// more than the whole sum.  Device time in us, one CTA / two kernels:
+//            T = 16      T = 48      T = 64      T = 96      T = 128     T = 160
+//   E = 64   4.6 / 6.7   4.8 / 6.1   5.0 / 6.2   5.9 / 6.6   6.0 / 7.1   6.9 / 7.7
+//   E = 256  5.2 / 7.3   5.5 / 7.3   5.8 / 7.4   7.1 / 7.6   7.2 / 7.6   8.4 / 8.0
+//   E = 512  3.5 / 7.6   5.7 / 7.6   6.8 / 7.7   8.8 / 7.9    11 / 7.8    13 / 8.3
+//   E = 1000 5.0 / 8.7   8.1 / 8.8   9.4 / 8.8    12 / 9.1    16 / 8.8    19 / 9.2
+// Several sequences go to two kernels: one CTA that walked them took a chain each (64
+// tokens, E = 128: in 2 sequences 10.6 against 8.6 us, in 16 67 against 12.4, in 128
+// 479 against 17.7).
+bool small_batch(int T, int E, int S) { return S == 1 && T <= (E <= 256 ? 128 : E <= 512 ? 64 : 48); }
 
 template <int VPL, bool VEC>
 __global__ void __launch_bounds__(VPL <= 8 ? 1024 : kThreads) balance_small_kernel(
     const float* __restrict__ logits, int T, int E, const int32_t* __restrict__ idx, int k,
-    const int32_t* __restrict__ seq, int S, const uint8_t* __restrict__ mask, int32_t* __restrict__ tokens,
-    float* __restrict__ loss, int32_t* __restrict__ counts, float* __restrict__ prob, float* __restrict__ coef,
-    int32_t* status) {
+    const int32_t* __restrict__ seq, const uint8_t* __restrict__ mask, float* __restrict__ loss,
+    int32_t* __restrict__ counts, float* __restrict__ prob, float* __restrict__ coef, int32_t* status) {
   extern __shared__ float smem[];
   const int threads = blockDim.x, warps = threads >> 5;
   float* wsum = smem;                                        // [warps][E]
@@ -324,55 +330,43 @@ __global__ void __launch_bounds__(VPL <= 8 ? 1024 : kThreads) balance_small_kern
   for (int e = threadIdx.x; e < E; e += threads) hist[e] = 0;
   pdl_wait();
   pdl_trigger();
-  double ball = 0, zall = 0;
-  int some = 0, all = 0;
-  for (int s = 0; s < S; ++s) {
-    int a = 0, b = T;
-    if (seq != nullptr) {
-      a = offset_at(seq, s, T);
-      b = offset_at(seq, s + 1, T);
-      if (threadIdx.x == 0 && (a > b || a != __ldg(seq + s) || b != __ldg(seq + s + 1))) report(status, MOE_ERR_DEVICE);
-    }
-    __syncthreads();                                         // hist is clear, wsum may be written
-    const Gathered<VPL> r = gather_tokens<VPL, VEC>(logits, E, idx, k, mask, a, b, warp, warps, lane, hist, status);
+  int a = 0, b = T;
+  if (seq != nullptr) {
+    a = offset_at(seq, 0, T);
+    b = offset_at(seq, 1, T);
+    if (threadIdx.x == 0 && (a > b || a != __ldg(seq) || b != __ldg(seq + 1))) report(status, MOE_ERR_DEVICE);
+  }
+  __syncthreads();                                           // hist is clear
+  const Gathered<VPL> r = gather_tokens<VPL, VEC>(logits, E, idx, k, mask, a, b, warp, warps, lane, hist, status);
 #pragma unroll
-    for (int j = 0; j < VPL; ++j)
-      if (expert_of<VEC>(j, lane) < E) wsum[warp * E + expert_of<VEC>(j, lane)] = r.acc[j];
-    if (lane == 0) {
-      wz[warp] = r.z;
-      wn[warp] = r.n;
-    }
-    __syncthreads();
-    double z = 0, q = 0;
-    int n = 0;
-    for (int w = 0; w < warps; ++w) {
-      z += wz[w];
-      n += wn[w];
-    }
-    for (int e = threadIdx.x; e < E; e += threads) {
-      double p = 0;
-      for (int w = 0; w < warps; ++w) p += wsum[w * E + e];
-      const int c = hist[e];
-      hist[e] = 0;
-      counts[static_cast<size_t>(s) * E + e] = c;
-      prob[static_cast<size_t>(s) * E + e] = n > 0 ? static_cast<float>(p / n) : 0.f;
-      q += p * c;
-    }
-    q = block_sum(q, shd);
-    if (threadIdx.x == 0) tokens[s] = n;
-    if (n > 0) ball += q * E / (static_cast<double>(k) * n * n);
-    zall += z;
-    some += n > 0;
-    all += n;
+  for (int j = 0; j < VPL; ++j)
+    if (expert_of<VEC>(j, lane) < E) wsum[warp * E + expert_of<VEC>(j, lane)] = r.acc[j];
+  if (lane == 0) {
+    wz[warp] = r.z;
+    wn[warp] = r.n;
   }
+  __syncthreads();
+  double z = 0, q = 0;
+  int n = 0;
+  for (int w = 0; w < warps; ++w) {
+    z += wz[w];
+    n += wn[w];
+  }
+  for (int e = threadIdx.x; e < E; e += threads) {
+    double p = 0;
+    for (int w = 0; w < warps; ++w) p += wsum[w * E + e];
+    const int c = hist[e];
+    counts[e] = c;
+    prob[e] = n > 0 ? static_cast<float>(p / n) : 0.f;
+    q += p * c;
+  }
+  q = block_sum(q, shd);
   if (threadIdx.x != 0) return;
-  for (int s = 0; s < S; ++s) {
-    const int n = tokens[s];
-    coef[s] = n > 0 ? static_cast<float>(E / (static_cast<double>(k) * n * n * some)) : 0.f;
-  }
-  coef[S] = 1.f / static_cast<float>(all > 0 ? all : 1);
-  loss[0] = some > 0 ? static_cast<float>(ball / some) : 0.f;
-  loss[1] = all > 0 ? static_cast<float>(zall / all) : 0.f;
+  const double factor = n > 0 ? E / (static_cast<double>(k) * n * n) : 0.0;
+  coef[0] = static_cast<float>(factor);
+  coef[1] = 1.f / static_cast<float>(n > 0 ? n : 1);
+  loss[0] = static_cast<float>(q * factor);
+  loss[1] = n > 0 ? static_cast<float>(z / n) : 0.f;
 }
 
 __global__ void __launch_bounds__(kThreads) balance_finish_kernel(
@@ -644,12 +638,12 @@ extern "C" moe_status moe_balance_loss(const float* logits, int T, int E, const 
   ws.sz = reinterpret_cast<double*>(w + L.sz);
   ws.ticket = reinterpret_cast<unsigned*>(w + L.ticket);
   const bool vec = E % 4 == 0 && aligned(logits, 16);
-  if (T <= kSmallTokens && S <= kSmallTokens) {
+  if (small_batch(T, E, S)) {
     const int warps = E <= 256 ? 32 : kWarps;   // registers: VPL <= 8 values a lane, or more
     const cudaError_t err = with_row(E, vec, [&](auto vpl, auto v) {
       return launch_pdl(balance_small_kernel<decltype(vpl)::value, decltype(v)::value>, dim3(1), dim3(warps * 32),
-                        static_cast<size_t>(warps + 1) * E * 4, stream, logits, T, E, idx, k, seq_offsets, S, mask,
-                        ws.sn, loss, counts, prob, coef, dev_status);
+                        static_cast<size_t>(warps + 1) * E * 4, stream, logits, T, E, idx, k, seq_offsets, mask, loss,
+                        counts, prob, coef, dev_status);
     });
     if (err != cudaSuccess) return fail(MOE_ERR_CUDA, "balance_small launch: %s", cudaGetErrorString(err));
     MOE_LAUNCH_CHECK("balance_small_kernel");

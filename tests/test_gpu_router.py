@@ -394,3 +394,43 @@ def test_the_status_word_lies_apart_from_the_outputs(moe):
     gap = wide.view(torch.int32).view(-1)[16:17]                       # between out's rows
     moe.moe_linear_w4(x, c, s, wide[:, :16], group=32, dev_status=gap)
     moe.moe_check_status(gap)
+
+
+@pytest.mark.parametrize("E", [20, 512, 516, 1000])
+def test_balance_where_one_cta_gives_way_to_two_kernels(moe, E):
+    """48, 64 and 128 tokens and one more, one sequence and two, by offsets or none."""
+    for T in (48, 49, 64, 65, 128, 129):
+        rng, l, idx, _ = routing(T, E, 4, 13)
+        mask = rng.random(T) < 0.8
+        l[~mask] = np.nan
+        for off in (None, [0, T], [3, T - 2], [T // 2, T // 2], [0, 5, T], [0, 0, T]):
+            check_balance(run_balance(moe, l, idx, off, mask), l, idx, off, mask)
+
+
+def test_balance_of_few_tokens_in_many_sequences_is_not_slow(moe):
+    """64 tokens in 64 sequences may not take 64 times those in one: they are 3 times
+    as slow in two kernels, 40 times where one CTA walks the sequences; 10 is between."""
+    _, l, idx, _ = routing(64, 128, 8, 14)
+    L, I = dev(l), dev(idx)
+    times = []
+    for S in (1, 64):
+        off = torch.arange(S + 1, dtype=torch.int32, device="cuda") * (64 // S)
+        o = [torch.empty(2, device="cuda"), torch.empty((S, 128), dtype=torch.int32, device="cuda"),
+             torch.empty((S, 128), device="cuda"), torch.empty(S + 1, device="cuda")]
+        ws = torch.empty(moe.moe_balance_loss_workspace_bytes(64, 128, S), dtype=torch.uint8, device="cuda")
+        moe.moe_balance_loss(L, I, *o, ws, seq_offsets=off)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            for _ in range(50):
+                moe.moe_balance_loss(L, I, *o, ws, seq_offsets=off)
+        best = float("inf")
+        for _ in range(10):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            g.replay()
+            b.record()
+            torch.cuda.synchronize()
+            best = min(best, a.elapsed_time(b))
+        times.append(best)
+    assert times[1] <= 10 * times[0], times
