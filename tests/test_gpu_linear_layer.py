@@ -324,3 +324,23 @@ def test_split_step_runs_the_shared_expert_beside_the_host_share(moe, monkeypatc
     monkeypatch.setattr(L, "moe_host_expert_ffn", slow_host)
     assert layer.split_step(0, logits.cuda(), x.cuda(), q=0.0, threads=2)["host"]
     assert seen == [True]
+
+
+@pytest.mark.parametrize("T", [3, 300])
+def test_fused_fp4_layer_with_a_shared_expert(moe, T):
+    """act="nvfp4" adds its experts into the output itself: with the shared expert (and a
+    host partial) it is the plain layer's output plus their sum, to fp32 rounding of
+    adds whose order may differ."""
+    cfg = synth.LayerConfig("nv", E=8, k=2, d=512, I=256, fmt="nvfp4", act="nvfp4")
+    b = Built(cfg, T, seed=6, act="nvfp4")
+    sh, wgu, wd = shared_expert("nvfp4", 16, 512, 192, T, seed=4)
+    from expert_offload_serving_b200.layer import MoeLayer
+    layer = MoeLayer(8, 512, 256, "nvfp4", 2, T, device_pool=b.layer.pool, act="nvfp4", shared=sh)
+    layer.slot.copy_(b.layer.slot)
+    logits, x, hp = b.logits.cuda(), b.x.cuda(), torch.randn((T, 512), device="cuda")
+    plain = b.layer.forward(logits, x).double().cpu().numpy()
+    a = torch.from_numpy(O.linear(b.x.double().numpy(), wgu, swiglu=True)).to(torch.bfloat16).double().numpy()
+    ref = plain + O.linear(a, wd)
+    check_tol(layer.forward(logits, x).cpu().numpy(), ref)
+    check_tol(layer.forward(logits, x, host_partial=hp).cpu().numpy(), ref + hp.double().cpu().numpy())
+    moe.moe_check_status(layer.status)

@@ -434,3 +434,11 @@ def test_balance_of_few_tokens_in_many_sequences_is_not_slow(moe):
             best = min(best, a.elapsed_time(b))
         times.append(best)
     assert times[1] <= 10 * times[0], times
+
+
+def test_no_tokens_in_several_sequences(moe):
+    l, idx = np.zeros((0, 24), dtype=np.float32), np.zeros((0, 3), dtype=np.int32)
+    check_balance(run_balance(moe, l, idx, [0, 0, 0, 0]), l, idx, [0, 0, 0, 0])
+    out = torch.empty((0, 24), device="cuda")
+    moe.moe_router_backward(dev(l), dev(idx), out, gate=torch.empty((0, 3), device="cuda"),
+                            dgate=torch.empty((0, 3), device="cuda"))
