@@ -167,7 +167,9 @@ __device__ __forceinline__ uint32_t pair_of(uint32_t w, uint32_t c) {
   }
 }
 constexpr uint32_t kMxBack = 0x7E807E80u;     // 2^126 twice
-constexpr float kNvPart = 1.298074214633707e33f, kNvBack = 65536.f;   // 2^110, 2^16 (a scale times 2^126 overflows)
+// 2^119 and 2^7: a scale of up to 448 times 2^126 overflows.  (The sums are 2^-7 of
+// their value until the end, so 7 bits are lost below fp32's normal range, no more.)
+constexpr float kNvPart = 6.646139978924579e35f, kNvBack = 128.f;
 
 // E8M0: 2^(b - 127); 0 is a subnormal of fp32, 255 is NaN.
 __device__ __forceinline__ float e8m0_value(uint32_t b) {

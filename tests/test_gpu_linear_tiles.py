@@ -183,3 +183,24 @@ def test_the_most_tokens_and_the_most_rows(moe, monkeypatch, path, T, N):
                         zeros=w["zeros"][n:n + (1 << 22)])
             y, S = products(part, x[t:t + (1 << 18)])
             check(out[t:t + (1 << 18), n:n + (1 << 22)], y, S, 32, "f32")
+
+
+@pytest.mark.parametrize("path", ["warp", "tc"])
+@pytest.mark.parametrize("fmt,group,zeros", FORMATS)
+def test_subnormal_x(moe, monkeypatch, path, fmt, group, zeros):
+    """x below the type's normal range counts with its value (a flushed one would be 0)."""
+    monkeypatch.setenv("MOE_LINEAR", path)
+    for xt, size in (("bf16", 2.0 ** -126), ("f16", 2.0 ** -14)):
+        for T in (5, 40):
+            w, g = make(fmt, group, zeros, 96, 512, 6)
+            x = (torch.randint(-127, 128, (T, 512), generator=g, device="cuda") * (size / 128)).to(DT[xt])
+            assert bool((x.float().abs() < size).all()) and bool((x != 0).any())
+            if fmt == "mxfp4":
+                w["scales"] += 127 + 30 - 115                          # the results are normal fp32 values
+            elif fmt == "nvfp4":
+                w["tensor_scale"] = 2.0 ** 30
+            else:
+                w["scales"] = (w["scales"].float() * 2.0 ** 40).to(torch.bfloat16)
+            out = torch.empty((T, 96), device="cuda")
+            call(moe, w, x, out)
+            check(out, *products(w, x), 512, "f32")
