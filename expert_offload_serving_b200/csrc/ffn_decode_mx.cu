@@ -922,18 +922,11 @@ moe_status launch_phase(const MxParams& P, const MxMaps& M, const DeviceInfo& de
 // is 128 codes x 128 rows, each 16 codes expanded into a 16-byte slot.
 CUresult encode_weight_map(CUtensorMap* map, const uint8_t* region0, int K, int R, int n_slots,
                            size_t blob_bytes) {
-  auto fn = encode_tiled_fn();
-  if (!fn) return CUDA_ERROR_NOT_FOUND;
-  const int KT = K / KSTAGE, RT = R / TM;
-  cuuint64_t gdim[5] = {static_cast<cuuint64_t>(KSTAGE), static_cast<cuuint64_t>(TM), static_cast<cuuint64_t>(KT),
-                        static_cast<cuuint64_t>(RT), static_cast<cuuint64_t>(n_slots)};
-  cuuint64_t gstr[4] = {128, static_cast<cuuint64_t>(kMxTileBytes),
-                        static_cast<cuuint64_t>(KT) * kMxTileBytes, static_cast<cuuint64_t>(blob_bytes)};
-  cuuint32_t box[5] = {128, static_cast<cuuint32_t>(TM), 1, 1, 1};
-  cuuint32_t estr[5] = {1, 1, 1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 5, const_cast<uint8_t*>(region0), gdim, gstr, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const uint64_t KT = K / KSTAGE, RT = R / TM;
+  const uint64_t dims[5] = {KSTAGE, TM, KT, RT, static_cast<uint64_t>(n_slots)};
+  const uint64_t strides[4] = {128, kMxTileBytes, KT * kMxTileBytes, blob_bytes};
+  const uint32_t box[5] = {128, TM, 1, 1, 1};
+  return encode_tiled_sw128(map, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 5, region0, dims, strides, box);
 }
 
 struct MxWorkspace {

@@ -381,63 +381,45 @@ inline CUresult with_context(F f) {
   return r;
 }
 
-// A tiled map with 128-byte swizzle: dims/strides in elements/bytes (strides
-// of dims 1..rank-1), box in elements; no interleave, zero fill out of bounds.
-// Returns a CUresult (CUDA_ERROR_NOT_FOUND when the entry point is missing).
+// A tiled map: dims/strides in elements/bytes (strides of dims 1..rank-1), box in
+// elements; no interleave, zero fill out of bounds.  Returns a CUresult
+// (CUDA_ERROR_NOT_FOUND when the entry point is missing).
+inline CUresult encode_tiled(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base,
+                             const uint64_t* dims, const uint64_t* strides, const uint32_t* box,
+                             CUtensorMapSwizzle swizzle, CUtensorMapL2promotion promotion) {
+  auto fn = encode_tiled_fn();
+  if (!fn) return CUDA_ERROR_NOT_FOUND;
+  cuuint64_t gdim[5], gstr[4];
+  cuuint32_t bx[5], estr[5];
+  for (int i = 0; i < rank; ++i) {
+    gdim[i] = dims[i];
+    bx[i] = box[i];
+    estr[i] = 1u;
+  }
+  for (int i = 0; i < rank - 1; ++i) gstr[i] = strides[i];
+  return with_context([&] {
+    return fn(map, type, rank, const_cast<void*>(base), gdim, gstr, bx, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+              promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  });
+}
+
+// With a 128-byte swizzle,
 inline CUresult encode_tiled_sw128(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base,
                                    const uint64_t* dims, const uint64_t* strides, const uint32_t* box) {
-  auto fn = encode_tiled_fn();
-  if (!fn) return CUDA_ERROR_NOT_FOUND;
-  cuuint64_t gdim[5], gstr[4];
-  cuuint32_t bx[5], estr[5];
-  for (int i = 0; i < rank; ++i) {
-    gdim[i] = dims[i];
-    bx[i] = box[i];
-    estr[i] = 1u;
-  }
-  for (int i = 0; i < rank - 1; ++i) gstr[i] = strides[i];
-  return with_context([&] {
-    return fn(map, type, rank, const_cast<void*>(base), gdim, gstr, bx, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  });
+  return encode_tiled(map, type, rank, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B,
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
-
-// The same with a 64-byte swizzle (inner box of 64 bytes).
+// a 64-byte swizzle (inner box of 64 bytes),
 inline CUresult encode_tiled_sw64(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base,
                                   const uint64_t* dims, const uint64_t* strides, const uint32_t* box) {
-  auto fn = encode_tiled_fn();
-  if (!fn) return CUDA_ERROR_NOT_FOUND;
-  cuuint64_t gdim[5], gstr[4];
-  cuuint32_t bx[5], estr[5];
-  for (int i = 0; i < rank; ++i) {
-    gdim[i] = dims[i];
-    bx[i] = box[i];
-    estr[i] = 1u;
-  }
-  for (int i = 0; i < rank - 1; ++i) gstr[i] = strides[i];
-  return with_context([&] {
-    return fn(map, type, rank, const_cast<void*>(base), gdim, gstr, bx, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  });
+  return encode_tiled(map, type, rank, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B,
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
-
-// The same without swizzle (rows land at the box's own pitch).
+// or none (rows land at the box's own pitch).
 inline CUresult encode_tiled_plain(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base,
                                    const uint64_t* dims, const uint64_t* strides, const uint32_t* box) {
-  auto fn = encode_tiled_fn();
-  if (!fn) return CUDA_ERROR_NOT_FOUND;
-  cuuint64_t gdim[5], gstr[4];
-  cuuint32_t bx[5], estr[5];
-  for (int i = 0; i < rank; ++i) {
-    gdim[i] = dims[i];
-    bx[i] = box[i];
-    estr[i] = 1u;
-  }
-  for (int i = 0; i < rank - 1; ++i) gstr[i] = strides[i];
-  return with_context([&] {
-    return fn(map, type, rank, const_cast<void*>(base), gdim, gstr, bx, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  });
+  return encode_tiled(map, type, rank, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE,
+                      CU_TENSOR_MAP_L2_PROMOTION_NONE);
 }
 
 }  // namespace tc

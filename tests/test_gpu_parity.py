@@ -376,3 +376,39 @@ def test_mxfp4_zero_block_with_smallest_scale_is_exact(moe):
     out = b.run().cpu().numpy()
     moe.moe_check_status(b.layer.status)
     check_tol(out, b.oracle()["out"], 1e-4, 1e-5)
+
+
+@pytest.mark.parametrize("fmt,act,T", [("bf16", "none", 8), ("mxfp4", "none", 8), ("mxfp4", "none", 40),
+                                       ("nvfp4", "none", 8), ("nvfp4", "nvfp4", 8), ("nvfp4", "nvfp4", 200)])
+def test_the_ffn_as_the_first_cuda_call_of_a_thread(moe, fmt, act, T):
+    """A thread that has made no CUDA call has no context bound; the tensor maps are
+    encoded all the same."""
+    import threading
+    cfg = synth.LayerConfig("thread", E=8, k=2, d=512, I=256, fmt=fmt, act=act)
+    b = Built(cfg, T, seed=3, act=act)
+    want, L_ = b.run().clone(), b.layer
+    x, out, y = b.x.cuda(), torch.zeros_like(want), None
+    if act == "none":
+        y = torch.zeros_like(L_.y_perm)
+    s = torch.cuda.current_stream().cuda_stream
+    torch.cuda.synchronize()
+    errors = []
+
+    def run():
+        try:
+            moe.moe_expert_ffn(L_.s, x, cfg.k, L_.offsets, L_.perm, L_.slot, L_.pool, L_.n_slots, y_perm=y,
+                               gate=None if act == "none" else L_.gate, out=None if act == "none" else out,
+                               flags=L_.flags, workspace=L_.workspace, dev_status=L_.status, stream=s)
+        except Exception as e:                                         # raised below, on the test's thread
+            errors.append(e)
+    t = threading.Thread(target=run)
+    t.start()
+    t.join()
+    if errors:
+        raise errors[0]
+    torch.cuda.synchronize()
+    moe.moe_check_status(L_.status)
+    if act == "none":
+        assert torch.equal(y, L_.y_perm)
+    else:                                                              # its atomics add in any order
+        check_tol(out.cpu().numpy(), want.double().cpu().numpy(), 1e-4, 1e-5)
