@@ -35,6 +35,7 @@
 // each, so that a thread's accumulators hold h and u of one output.
 #pragma once
 
+#include <atomic>
 #include <type_traits>
 
 #include <cuda_bf16.h>
@@ -531,11 +532,11 @@ template <int FMT, int GROUP, bool BF16, int NT, int RT>
 cudaError_t launch(LinearParams P, const DeviceInfo& dev, cudaStream_t s) {
   using G = Geometry<FMT, GROUP, BF16, NT, RT>;
   auto kern = linear_w4_kernel<FMT, GROUP, BF16, NT, RT>;
-  static bool done[64] = {};
-  if (!done[dev.id]) {
+  static std::atomic<bool> done[64];
+  if (!done[dev.id].load(std::memory_order_acquire)) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
     if (e != cudaSuccess) return e;
-    done[dev.id] = true;
+    done[dev.id].store(true, std::memory_order_release);
   }
   const int tiles = (P.N + 15) / 16;
   // Rows per CTA: the most that still give the SMs a CTA and a half each.  Fewer

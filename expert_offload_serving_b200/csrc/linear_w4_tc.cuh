@@ -153,8 +153,7 @@ __device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
 }
 template <int N>
 __device__ __forceinline__ void tmem_load(uint32_t taddr, float (&v)[N]) {
-  if constexpr (N == 4) tmem_ld4(taddr, v);
-  else if constexpr (N == 8) tmem_ld8(taddr, v);
+  if constexpr (N == 8) tmem_ld8(taddr, v);
   else if constexpr (N == 16) tmem_ld16(taddr, v);
   else tmem_ld32(taddr, v);
 }

@@ -423,11 +423,11 @@ template <int FMT, int GROUP, bool BF16>
 cudaError_t launch(const LinearParams& P, const DeviceInfo& dev, int32_t* status, cudaStream_t s) {
   using C = Cfg<FMT, GROUP>;
   auto kern = linear_w4_tc16_kernel<FMT, GROUP, BF16>;
-  static bool done[64] = {};
-  if (!done[dev.id]) {
+  static std::atomic<bool> done[64];
+  if (!done[dev.id].load(std::memory_order_acquire)) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
-    done[dev.id] = true;
+    done[dev.id].store(true, std::memory_order_release);
   }
   TcParams Q{};
   Q.L = P;

@@ -5,13 +5,11 @@
 namespace moe {
 namespace {
 
-// Up to 16 tokens the narrow kernel, for the formats that it is the faster one for.
-template <int FMT, int GROUP, bool BF16>
-cudaError_t launch(const LinearParams& P, const DeviceInfo& dev, int32_t* status, cudaStream_t s) {
-  if constexpr (FMT == MOE_W_MXFP4 || (FMT == MOE_W_INT4 && GROUP >= 64)) {
-    if (P.T <= w4t16::NT) return w4t16::launch<FMT, GROUP, BF16>(P, dev, status, s);
-  }
-  return w4tc::launch_tokens<FMT, GROUP, BF16>(P, dev, status, s);
+// MXFP4: up to 16 tokens the narrow kernel, which is the faster one for it.
+template <bool BF16>
+cudaError_t launch_mxfp4(const LinearParams& P, const DeviceInfo& dev, int32_t* status, cudaStream_t s) {
+  return P.T <= w4t16::NT ? w4t16::launch<MOE_W_MXFP4, 32, BF16>(P, dev, status, s)
+                          : w4tc::launch_tokens<MOE_W_MXFP4, 32, BF16>(P, dev, status, s);
 }
 
 }  // namespace
@@ -19,8 +17,9 @@ cudaError_t launch(const LinearParams& P, const DeviceInfo& dev, int32_t* status
 cudaError_t launch_linear_tc_fp4(const LinearParams& P, int fmt, bool bf16, const DeviceInfo& dev, int32_t* status,
                                  cudaStream_t s) {
   if (fmt == MOE_W_MXFP4)
-    return bf16 ? launch<MOE_W_MXFP4, 32, true>(P, dev, status, s) : launch<MOE_W_MXFP4, 32, false>(P, dev, status, s);
-  return bf16 ? launch<MOE_W_NVFP4, 16, true>(P, dev, status, s) : launch<MOE_W_NVFP4, 16, false>(P, dev, status, s);
+    return bf16 ? launch_mxfp4<true>(P, dev, status, s) : launch_mxfp4<false>(P, dev, status, s);
+  return bf16 ? w4tc::launch_tokens<MOE_W_NVFP4, 16, true>(P, dev, status, s)
+              : w4tc::launch_tokens<MOE_W_NVFP4, 16, false>(P, dev, status, s);
 }
 
 }  // namespace moe
