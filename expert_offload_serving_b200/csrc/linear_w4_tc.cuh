@@ -76,13 +76,6 @@ struct TcParams {
   uint64_t wait_ns;
   int stall, mt, tt;                          // tiles of rows, of tokens
   int ck_bits;                                // CTAs of a cluster that share a tile's K (log2)
-  // PRE: stages whose products run through one accumulator (log2).  The tensor cores
-  // cut sums off instead of rounding them: K = 16384 in two planes through one
-  // accumulator is off by 2.4e-6 of the result's norm.  For an fp32 y the sums are
-  // added in registers after 8 stages (4.8e-7; 7 % of the time at NT = 64, 20 % at
-  // 128, whose sets have a single accumulator), a 16-bit y does not notice and they
-  // run on.
-  int run_bits;
   int32_t* status;
 };
 
@@ -190,10 +183,18 @@ __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile
   return mbar_wait<false>(bar, parity, abort_flag, limit_ns);
 }
 
+// PRE: stages whose products run through one accumulator.  The tensor cores cut sums
+// off instead of rounding them: K = 16384 in two planes through one accumulator is off
+// by 7.7e-6 of the result's norm (2.4e-6 where a cluster shares it).  For an fp32 y
+// the sums are added in registers after 8 stages (4.8e-7); a 16-bit y does not notice
+// and they run on.
+constexpr int kRun = 8;
+
 // SHARED: a cluster of CTAs shares a tile's K.  RUNS: PRE sums are added in registers
 // after each run.  (Instances of their own: the few more instructions of SHARED made
-// the loops of the other one 12 % slower at NT = 64, the sums that RUNS holds across
-// them 14 % at NT = 128.)
+// the loops of the other one 12 % slower at NT = 64, and the sums that RUNS holds
+// across them cost 8 % at NT = 32 and 64 and 14 % at 128.  T = 64, N = 16384, K = 4096,
+// INT4 by 128: 23.6 us without, 25.4 with.)
 template <int FMT, int GROUP, bool BF16, int NT, bool POST, bool SHARED, bool RUNS>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
@@ -219,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int rank = SHARED ? static_cast<int>(cluster_rank()) : 0;
   const int all = (P.K + KS - 1) / KS, s0 = all * rank >> ck_bits, nst = (all * (rank + 1) >> ck_bits) - s0;
   const int ntiles = Q.mt * Q.tt, tile0 = blockIdx.x >> ck_bits, tiles_step = gridDim.x >> ck_bits;
-  const int run = POST ? 1 : 1 << (RUNS ? Q.run_bits : 30);
+  constexpr int run = POST ? 1 : RUNS ? kRun : 1 << 30;
   int meetings = 0;                           // barriers over the cluster: two, on every path
   const int outs = P.swiglu ? P.N >> 1 : P.N, per = P.swiglu ? TM / 2 : TM;   // outputs: in all, of a tile
 
@@ -505,7 +506,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Stages up to s - 2 are added up before the wait for the buffer that stage
         // s - 2's MMAs read: these may in turn wait for accumulators (a stage can
         // have more groups than there are accumulators).
-        for (; (POST || RUNS) && next * run + run < s && ok; ++next) ok = POST ? add_up(next) : add_run(next);
+        if constexpr (POST || RUNS)
+          for (; next * run + run < s && ok; ++next) ok = POST ? add_up(next) : add_run(next);
         uint32_t c[HC], s1[HC], s2[HC];
 #pragma unroll
         for (int i = 0; i < HC; ++i) {
@@ -585,7 +587,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         arrive(&afull[set]);
       }
-      for (; next * run < nst && ok; ++next) ok = POST ? add_up(next) : add_run(next);
+      if constexpr (POST || RUNS) {
+        for (; next * run < nst && ok; ++next) ok = POST ? add_up(next) : add_run(next);
+      } else {
+        ok = ok && add_run(0);
+      }
       if (!ok) break;
       // y[t][n] of tokens i and i + 1 of this thread: lanes hold consecutive n
       const int n = first + out_row;
@@ -697,7 +703,6 @@ cudaError_t launch(const LinearParams& P, const DeviceInfo& dev, int32_t* status
   Q.wait_ns = wait_limit_ns();
   Q.stall = test_stall();
   Q.status = status;
-  Q.run_bits = P.y_f32 ? 3 : 30;
   using C = Cfg<FMT, GROUP, BF16, NT, POST>;
   constexpr int A = C::GPS > C::HC ? C::GPS : C::HC;                   // groups that are loaded at once
   const int e = FMT != MOE_W_INT4 ? 1 : P.scale_type == MOE_DT_F32 ? 4 : 2;
@@ -720,7 +725,7 @@ cudaError_t launch(const LinearParams& P, const DeviceInfo& dev, int32_t* status
   // four stages.
   const int nst = (P.K + KS - 1) / KS;
   while (Q.ck_bits < 3 && tiles << (Q.ck_bits + 1) <= dev.sm_count && nst >> (Q.ck_bits + 1) >= 4) ++Q.ck_bits;
-  if constexpr (!POST && NT == 128) {
+  if constexpr (!POST) {
     if (!P.y_f32)
       return Q.ck_bits > 0 ? launch_tiles<FMT, GROUP, BF16, NT, POST, true, false>(Q, tm_w, tm_x, tiles, dev, s)
                            : launch_tiles<FMT, GROUP, BF16, NT, POST, false, false>(Q, tm_w, tm_x, tiles, dev, s);
