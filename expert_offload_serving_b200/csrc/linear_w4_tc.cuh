@@ -194,7 +194,7 @@ constexpr int kRun = 8;
 // after each run.  (Instances of their own: the few more instructions of SHARED made
 // the loops of the other one 12 % slower at NT = 64, and the sums that RUNS holds
 // across them cost 8 % at NT = 32 and 64 and 14 % at 128.  T = 64, N = 16384, K = 4096,
-// INT4 by 128: 23.6 us without, 25.4 with.)
+// INT4 by 128: 23.3 us without, 25.4 with.)
 template <int FMT, int GROUP, bool BF16, int NT, bool POST, bool SHARED, bool RUNS>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
@@ -587,11 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         arrive(&afull[set]);
       }
-      if constexpr (POST || RUNS) {
-        for (; next * run < nst && ok; ++next) ok = POST ? add_up(next) : add_run(next);
-      } else {
-        ok = ok && add_run(0);
-      }
+      for (; next * run < nst && ok; ++next) ok = POST ? add_up(next) : add_run(next);
       if (!ok) break;
       // y[t][n] of tokens i and i + 1 of this thread: lanes hold consecutive n
       const int n = first + out_row;
