@@ -16,15 +16,16 @@
 //
 // Few tokens of one sequence: one CTA does it all (5.3 us at T = 64, E = 128, k = 8);
 // the latency of its steps bounds it.  T = 50000, E = 256, k = 6 in 29 sequences, a tenth
-// masked: 20.7 us (2.3 TB/s), some 13 in the first kernel, bound by instructions (a
-// softmax and the sums of 8 values a lane), the rest the second one's chain of
-// dependent loads.  Cut into 592 tiles 23.9 us, 296 25.9, 1184 24.2 (with the calls'
+// masked: 22.7 us (2.1 TB/s) on inputs in turn, 20.7 on the same ones, some 13 in the
+// first kernel, bound by instructions (a softmax and the sums of 8 values a lane), the
+// rest the second one's chain of dependent loads.  Cut into 592 tiles 23.9 us, 296 25.9, 1184 24.2 (with the calls'
 // gaps).
 //
 // Backward: one warp per token, nothing kept from the forward but counts and
 // coef: the softmax is formed again from the logits, which costs no traffic
 // (the row is read anyway): 4 E bytes in, 4 E out per token.  T = 50000, E = 256:
-// 23.9 us, 4.2 TB/s; instructions bound it (2.5 a clock of an SM), HBM's share is 15.
+// 28.6 us on inputs in turn, 3.5 TB/s (25 on the same ones); instructions bound it (2.5
+// a clock of an SM), HBM's share is 15.
 // 4 tokens a warp; 2 took as long, 1 and 8 13 % longer.
 #include <climits>
 #include <cmath>

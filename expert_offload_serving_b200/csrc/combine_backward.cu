@@ -6,9 +6,10 @@
 // A CTA per pair: it reads the pair's y row and writes its dy row, and reads its
 // token's dout row, which the token's other pairs find in L2.  Bound by HBM: per
 // token (k + 1) rows read and k written.  Against a CTA per token with 8 pairs at
-// once (dout read once, 128 registers): 100 against 121 us at T = 4096, k = 6,
-// d = 4096 (6.3 against 5.2 TB/s of the 631 MB; HBM bounds it), 2.4 against 7.3 us
-// at T = 16, k = 8, d = 2048 (the launch and three dependent loads).  y and dy pass through the caches once and are marked so.  A
+// once (dout read once, 128 registers): 104 against 121 us at T = 4096, k = 6,
+// d = 4096 (6.1 against 5.2 TB/s of the 631 MB; HBM bounds it; without dy 64.5 us, 5.4
+// TB/s of 349 MB), 2.4 against 7.3 us at T = 16, k = 8, d = 2048 (the launch and three
+// dependent loads).  y and dy pass through the caches once and are marked so.  A
 // dot is summed in fp32: per thread over its columns, then over the lanes of a
 // warp, then over the warps -- a fixed order.
 #include "common.cuh"

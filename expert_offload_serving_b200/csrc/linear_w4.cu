@@ -13,7 +13,7 @@ namespace {
 // share that chain where tiles are few; up to 16, enough tiles to fill the SMs pay
 // for it.  Groups of 32 whose sums are scaled (f16 x; fp32 scales with an fp32 y) have
 // four hand-overs a stage, which 32 tokens do not pay for either.  Device time in us,
-// warp / tcgen05, K = 4096 (weights of N <= 16384 in L2):
+// warp / tcgen05, fp32 y, K = 4096 (weights of N <= 16384 in L2):
 //   bf16 x               INT4/128      INT4/32       MXFP4         NVFP4         f16 x: INT4/32
 //   T = 8   N = 16384   14.5 / 17.8   22.7 / 25.7   24.3 / 26.4   22.9 / 25.5   22.7 / 44.5
 //   T = 16  N = 4096     9.0 / 17.6   10.9 / 10.6   10.8 / 26.0   10.0 / 10.1   10.8 / 15.5

@@ -22,10 +22,11 @@
 // and the words of x are permuted alike; where E2M1 converts to f16 by the byte,
 // the pairs are (k, k+1), ... and x stays as it is.
 //
-// What bounds it: few tokens, the latency of a launch and of K's chain of stages
+// What bounds it: few tokens, the latency of a launch and of the one or two stages that
+// a CTA then has, none of which is multiplied before it has landed whole
 // (T = 1, N = 2048, K = 768: 2.8 us, of which the 0.8 MB take 0.13 at the copy rate;
-// T = 1 with N = 4096, K = 4096 of MXFP4: 7.0 us, 1.3 TB/s; T = 8, N = 4096, K = 2048
-// of NVFP4: 5.2 us); many rows, instructions: 4 to 6 a pair of weights at two a
+// T = 1 with N = 4096, K = 4096 of MXFP4, 256 CTAs of two stages: 7.0 us, 1.3 TB/s;
+// T = 8, N = 4096, K = 2048 of NVFP4, one stage: 4.9 us); many rows, instructions: 4 to 6 a pair of weights at two a
 // clock for an SM (T = 4, N = 131072, K = 4096, INT4 by 128: 92 us, 3.0 TB/s).  K is
 // split over warps rather than CTAs (their sums meet in shared memory, one launch);
 // 8 warps of 16 rows, two CTAs an SM, gave the shortest chain.

@@ -29,9 +29,9 @@
 // each adds up, out of the others' shared memory and in their order, the sums of a
 // part of the tokens.
 //
-// Measured: T = 64, N = 16384, K = 4096, INT4 by 128: 25 us (344 TFLOP/s, 687 with
-// both planes; one set of eight warps took 44).  T = 1000, N = K = 4096 with SwiGLU,
-// INT4 by 32: 69 us (487, 974 with both planes), by 128 62 us.  T = 64, N = 1024: 8.7
+// Measured, bf16 y: T = 64, N = 16384, K = 4096, INT4 by 128: 23.3 us (369 TFLOP/s, 737
+// with both planes; one set of eight warps took 44).  T = 1000, N = K = 4096 with SwiGLU,
+// INT4 by 32: 67 us (498, 996 with both planes), by 128 60.5 us.  T = 64, N = 1024: 8.1
 // us by clusters of 8.  A tile takes some 3 to 8 us beside its stages (first loads,
 // draining, epilogue), a stage of 64 tokens 1200 cycles and one of 128 1350 to 1550,
 // of which the two planes' MMAs are 512 and 1024 and the expanding instructions 640

@@ -453,12 +453,13 @@ moe_status moe_profile_bandwidth(moe_shape s, const void* host_pool, int n_blobs
  *            overlap x or the weights, nor dev_status any of them.
  * Products are exact, sums are fp32 in a fixed order (the same call gives the same
  * bits), y is rounded once.  (Two exceptions on the tcgen05 kernels, INT4 with bf16 x:
- * for a bf16 y, fp32 scales leave a weight within 2^-14.8 of itself; and unless the
- * scales are fp32 and y is too, a weight above 2^127 may count as infinite.)  (The tensor cores cut off where fp32
- * would round: 2.4e-6 of the result's norm at K = 16384, measured.  For an fp32 y
- * the kernels therefore add up in registers after at most 1024 of K; for a 16-bit
- * y, whose own rounding is 100 times that, some sums run through all of K.)  An infinity or NaN
- * in a row of x makes that row of y infinite or NaN and no other.
+ * for a bf16 y, fp32 scales leave a weight within 2^-14.8 of itself; and unless scales
+ * and y are both fp32, a weight (code - zero) * scale of 2^127 or more may make its
+ * output infinite or NaN.)  The tensor cores cut off where fp32 would round: up to 8e-6
+ * of the result's norm at K = 16384, measured.  For an fp32 y the kernels therefore add
+ * up in registers after at most 1024 of K (below 1e-6); for a 16-bit y, whose own
+ * rounding is 100 times that, some sums run through all of K.  An infinity or NaN in a
+ * row of x makes that row of y infinite or NaN and no other.
  *   dev_status: device int32 word or NULL; MOE_ERR_TIMEOUT is recorded there if a
  * bounded wait of the tcgen05 kernels runs out (y is then incomplete).  Warp-level
  * or tcgen05 kernels are chosen by T, N and the format; the environment variable
