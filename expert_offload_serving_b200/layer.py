@@ -180,7 +180,8 @@ class MoeLayer:
         self.status = torch.zeros((1,), **i32)
         # The slots of the last step, for its gradient (_keep_slots); None: the table's own
         self.step_slot = None
-        self._step_slot = None if act == "nvfp4" else torch.empty((E,), **i32)
+        with torch.inference_mode(False):    # written by torch, within that mode and outside of it
+            self._step_slot = None if act == "nvfp4" else torch.empty((E,), **i32)
         self._host_steps = False             # whether any step (one that a graph replays, too) merged a host partial
         self.shared = shared
         if shared is not None:

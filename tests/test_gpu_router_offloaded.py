@@ -206,3 +206,18 @@ def test_logits_and_balance_of_another_shape_are_refused(moe):
     with pytest.raises(ValueError, match="coef"):
         layer.router_grad(logits, balance=dict(bal, coef=bal2["coef"]), dloss=dloss)
     layer.router_grad(logits, balance=bal2, dloss=dloss, seq_offsets=off)
+
+
+@pytest.mark.parametrize("inside", [True, False])
+def test_layer_built_in_inference_mode(moe, inside):
+    """Its steps run within that mode and outside of it."""
+    with torch.inference_mode():
+        c = Cached()
+    layer, (logits, x, dout) = c.layers[0], c.in_[0]
+    hp = torch.zeros((T, D), device="cuda")
+    with torch.inference_mode(inside):
+        c.prepare(0, c.chosen(0))
+        want = layer.forward(logits, x).clone()
+        got = layer.router_grad(logits, dout)
+        assert torch.equal(layer.forward(logits, x, host_partial=hp), want)
+        assert torch.equal(layer.router_grad(logits, dout), got)
