@@ -531,7 +531,9 @@ moe_status moe_router_backward(const float* logits, int T, int E, const int32_t*
  * adds (same rules on slot_of_expert and inv_perm), with q = inv_perm[p],
  *   dgate[t][j] = sum_c dout[t][c] y_perm[q][c]      dy_perm[q][c] = gate[t][j] dout[t][c]
  * and dgate[t][j] = 0 for the others, whose rows of dy_perm are left as they were.
- * (The gradient of host_partial is dout itself.)  dout fp32 [T][d]; dgate fp32
+ * slot_of_expert is the table as the step's combine read it: a cache's fills change it, so a
+ * gradient formed later needs a copy.  Pairs computed on the host have no y_perm row, and
+ * their dgate is 0 here.  (The gradient of host_partial is dout itself.)  dout fp32 [T][d]; dgate fp32
  * [T][k]; dy_perm fp32 [T*k][d] or NULL (not wanted; gate is then not read).  Both
  * overlap neither each other nor an input. */
 moe_status moe_combine_backward(const float* y_perm, const int32_t* idx, const float* gate,
